@@ -6,5 +6,5 @@ The compute lives in liboda.so (CUDA for sm_100a, C ABI in include/oda.h);
 
 from .oda import (  # noqa: F401
     BF16, F32, EXPORTS, LIB_PATH, MAX_BATCH, OdaConfig, OdaContext, OdaError, OdaGraph,
-    OdaStepDesc, layout, lib, make_config, ptr, version,
+    OdaStepDesc, kv8_layout, layout, lib, make_config, ptr, version,
 )

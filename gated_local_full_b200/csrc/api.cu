@@ -38,6 +38,43 @@ oda_status check_batch(const oda_ctx* ctx, int B) {
   return ODA_OK;
 }
 
+// What the 8-bit cache's entry points share: the format, the device.
+oda_status check_device(const oda_ctx* ctx) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ODA_ERR_CUDA;
+  return dev == ctx->device ? ODA_OK : ODA_ERR_STATE;
+}
+
+oda_status check_kv8(const oda_ctx* ctx, int format) {
+  if (format != ODA_KV8_INT8 && format != ODA_KV8_E4M3) return ODA_ERR_DTYPE;
+  return check_device(ctx);
+}
+
+bool aligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+oda_status attn_kv8(oda_ctx* ctx, int format, int layer, const void* q, const int32_t* seq_lens,
+                    const int32_t* range_lo, const int32_t* range_hi, const int32_t* block_table,
+                    const void* codes, const float* scales, const int32_t* idx,
+                    const int32_t* count, void* out, float* lse, int B, unsigned flags,
+                    oda_stream stream) {
+  if (!ctx) return ODA_ERR_ARG;
+  oda_status s = check_batch(ctx, B);
+  if (s == ODA_OK) s = check_kv8(ctx, format);
+  if (s != ODA_OK) return s;
+  if (layer < 0 || layer >= ctx->cfg.layers) return ODA_ERR_ARG;
+  if (flags & ~ODA_ATTN_INPUTS_READY) return ODA_ERR_ARG;
+  if (B == 0) return ODA_OK;
+  if (!q || !seq_lens || !block_table || !codes || !scales || !idx || !count || !out)
+    return ODA_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(codes, 16) || !aligned(scales, 8))
+    return ODA_ERR_ARG;
+  return oda_impl::launch_attn_kv8(ctx, format, layer, q, seq_lens, range_lo, range_hi,
+                                   block_table, codes, scales, idx, count, out, lse, B,
+                                   static_cast<cudaStream_t>(stream));
+}
+
 __global__ void wait_selftest_kernel(uint64_t timeout_ns, int* err) {
   __shared__ uint64_t bar;
   if (threadIdx.x == 0) {
@@ -150,10 +187,12 @@ oda_status oda_create(const oda_config* cfg, oda_ctx** out) {
     return ODA_ERR_CUDA;
   }
   s = oda_impl::attn_setup(ctx);
+  if (s == ODA_OK) s = oda_impl::attn_kv8_setup(ctx);
   if (s == ODA_OK) {
     const int g = cfg->hq / cfg->hkv;
-    const int ctas = ctx->attn_ctas_local > ctx->attn_ctas_full ? ctx->attn_ctas_local
-                                                                : ctx->attn_ctas_full;
+    int ctas = ctx->attn_ctas_local > ctx->attn_ctas_full ? ctx->attn_ctas_local
+                                                          : ctx->attn_ctas_full;
+    if (ctx->attn_kv8_ctas > ctas) ctas = ctx->attn_kv8_ctas;
     ctx->max_parts = ctas + cfg->max_batch * cfg->hkv;
     const size_t pbytes = (size_t)ctx->max_parts * g * (cfg->head_dim + 2) * sizeof(float);
     if (cudaMalloc(&ctx->partials, pbytes) != cudaSuccess ||
@@ -324,6 +363,107 @@ oda_status oda_gate(oda_ctx* ctx, const float* scores, float theta, int B, uint8
   if (!count || (B > 0 && (!scores || !flags || !idx))) return ODA_ERR_ARG;
   return oda_impl::launch_gate(ctx, scores, theta, B, flags, idx, count,
                                static_cast<cudaStream_t>(stream), 0ull, false);
+}
+
+oda_status oda_kv8_layout(const oda_config* cfg, oda_kv8_layout_info* out) {
+  if (!out) return ODA_ERR_ARG;
+  const oda_status s = check_config(cfg);
+  if (s != ODA_OK) return s;
+  out->tile_bytes = 2ll * ODA_TILE * cfg->head_dim;
+  out->cache_layer_bytes = cfg->num_blocks * cfg->hkv * out->tile_bytes;
+  out->scale_layer_elems = cfg->num_blocks * cfg->hkv * 2;
+  return ODA_OK;
+}
+
+oda_status oda_append_kv8(oda_ctx* ctx, int format, int layer_begin, int layer_end,
+                          const void* k_new, const void* v_new, const int32_t* tok_start,
+                          int64_t n_tokens, const int32_t* seq_lens, const int32_t* block_table,
+                          void* codes, float* scales, void* ring, int B, oda_stream stream) {
+  if (!ctx) return ODA_ERR_ARG;
+  oda_status s = check_batch(ctx, B);
+  if (s == ODA_OK) s = check_kv8(ctx, format);
+  if (s != ODA_OK) return s;
+  if (layer_begin < 0 || layer_end > ctx->cfg.layers || layer_begin > layer_end) return ODA_ERR_ARG;
+  if (n_tokens < 0 || (!tok_start && n_tokens != B)) return ODA_ERR_ARG;
+  if (n_tokens > (int64_t)INT32_MAX) return ODA_ERR_SHAPE;
+  if (B == 0 || n_tokens == 0 || layer_begin == layer_end) return ODA_OK;
+  if (!k_new || !v_new || !seq_lens || !block_table || !codes || !scales) return ODA_ERR_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(codes, 16) || !aligned(scales, 8) ||
+      !aligned(ring, 16))
+    return ODA_ERR_ARG;
+  return oda_impl::launch_append_kv8(ctx, format, layer_begin, layer_end, k_new, v_new, tok_start,
+                                     n_tokens, seq_lens, block_table, codes, scales, ring, B,
+                                     static_cast<cudaStream_t>(stream));
+}
+
+oda_status oda_read_kv8(oda_ctx* ctx, int format, int layer_begin, int layer_end,
+                        const int32_t* tok_start, int64_t n_tokens, const int32_t* seq_lens,
+                        const int32_t* block_table, const void* codes, const float* scales,
+                        void* k_out, void* v_out, int B, oda_stream stream) {
+  if (!ctx) return ODA_ERR_ARG;
+  oda_status s = check_batch(ctx, B);
+  if (s == ODA_OK) s = check_kv8(ctx, format);
+  if (s != ODA_OK) return s;
+  if (layer_begin < 0 || layer_end > ctx->cfg.layers || layer_begin > layer_end) return ODA_ERR_ARG;
+  if (n_tokens < 0 || (!tok_start && n_tokens != B)) return ODA_ERR_ARG;
+  if (n_tokens > (int64_t)INT32_MAX) return ODA_ERR_SHAPE;
+  if (B == 0 || n_tokens == 0 || layer_begin == layer_end || (!k_out && !v_out)) return ODA_OK;
+  if (!seq_lens || !block_table || !codes || !scales) return ODA_ERR_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(codes, 16) || !aligned(scales, 8))
+    return ODA_ERR_ARG;
+  return oda_impl::launch_read_kv8(ctx, format, layer_begin, layer_end, tok_start, n_tokens,
+                                   seq_lens, block_table, codes, scales, k_out, v_out, B,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+oda_status oda_full_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
+                             const int32_t* seq_lens, const int32_t* block_table,
+                             const void* codes, const float* scales, const int32_t* idx,
+                             const int32_t* count, void* out, float* lse, int B, unsigned flags,
+                             oda_stream stream) {
+  return attn_kv8(ctx, format, layer, q, seq_lens, nullptr, nullptr, block_table, codes, scales,
+                  idx, count, out, lse, B, flags, stream);
+}
+
+oda_status oda_range_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
+                              const int32_t* seq_lens, const int32_t* range_lo,
+                              const int32_t* range_hi, const int32_t* block_table,
+                              const void* codes, const float* scales, const int32_t* idx,
+                              const int32_t* count, void* out, float* lse, int B, unsigned flags,
+                              oda_stream stream) {
+  if (B > 0 && (!range_lo || !range_hi)) return ODA_ERR_ARG;
+  return attn_kv8(ctx, format, layer, q, seq_lens, range_lo, range_hi, block_table, codes, scales,
+                  idx, count, out, lse, B, flags, stream);
+}
+
+oda_status oda_qk_norm_rope(oda_ctx* ctx, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* q_weight, const void* k_weight,
+                            float eps, const float* inv_freq, int rot_dim,
+                            const int32_t* positions, int pos_offset, int64_t n, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            unsigned flags, oda_stream stream) {
+  if (!ctx || n < 0 || (flags & ~ODA_ROPE_NEIGHBOURS)) return ODA_ERR_ARG;
+  const oda_config& c = ctx->cfg;
+  oda_status s = check_device(ctx);
+  if (s != ODA_OK) return s;
+  if (!(eps >= 0.f)) return ODA_ERR_ARG;             // a NaN too
+  if (rot_dim < 0 || rot_dim > c.head_dim || rot_dim % 16 != 0) return ODA_ERR_SHAPE;
+  if (n > (int64_t)INT32_MAX) return ODA_ERR_SHAPE;
+  if (n == 0) return ODA_OK;
+  if (!q || !q_out || (rot_dim > 0 && (!inv_freq || !positions))) return ODA_ERR_ARG;
+  if ((k == nullptr) != (k_out == nullptr)) return ODA_ERR_ARG;
+  const int64_t qe = (int64_t)c.hq * c.head_dim, ke = (int64_t)c.hkv * c.head_dim;
+  const int64_t m = 16 / ctx->lay.elem_bytes;
+  if (q_stride < qe || q_out_stride < qe || q_stride % m || q_out_stride % m) return ODA_ERR_SHAPE;
+  if (k && (k_stride < ke || k_out_stride < ke || k_stride % m || k_out_stride % m))
+    return ODA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return ODA_ERR_ARG;
+  return oda_impl::launch_qk_norm_rope(ctx, q, q_stride, k, k_stride, q_weight, k_weight, eps,
+                                       inv_freq, rot_dim, (flags & ODA_ROPE_NEIGHBOURS) != 0,
+                                       positions, pos_offset, n, q_out, q_out_stride, k_out,
+                                       k_out_stride, static_cast<cudaStream_t>(stream));
 }
 
 oda_status oda_get_device_error(oda_ctx* ctx, oda_stream stream, int* err) {

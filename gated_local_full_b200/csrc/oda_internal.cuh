@@ -18,6 +18,7 @@ struct oda_ctx {
   int num_sms;
   int attn_ctas_local;       // persistent grid of the Local attention kernel
   int attn_ctas_full;        // persistent grid of the Full attention kernel
+  int attn_kv8_ctas;         // persistent grid of the attention over the 8-bit cache
   int max_parts;             // capacity of the partials buffer (in partials)
   float* partials;           // [max_parts][G][d+2]
   int* tickets;              // [2][max_batch * hkv]: merge tickets, dynamic tile counters;
@@ -274,6 +275,26 @@ oda_status launch_recall_loss(oda_ctx* ctx, const float* q, const float* lpf, co
                               float lam, long long n, float* loss, int32_t* n_full,
                               cudaStream_t st);
 oda_status launch_wait_selftest(oda_ctx* ctx, uint64_t timeout_ns, cudaStream_t st);
+oda_status attn_kv8_setup(oda_ctx* ctx);
+oda_status launch_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
+                           const int32_t* seq_lens, const int32_t* range_lo,
+                           const int32_t* range_hi, const int32_t* block_table, const void* codes,
+                           const float* scales, const int32_t* idx, const int32_t* count, void* out,
+                           float* lse, int B, cudaStream_t st);
+oda_status launch_append_kv8(oda_ctx* ctx, int format, int lb, int le, const void* k_new,
+                             const void* v_new, const int32_t* tok_start, long long n_tokens,
+                             const int32_t* seq_lens, const int32_t* block_table, void* codes,
+                             float* scales, void* ring, int B, cudaStream_t st);
+oda_status launch_read_kv8(oda_ctx* ctx, int format, int lb, int le, const int32_t* tok_start,
+                           long long n_tokens, const int32_t* seq_lens, const int32_t* block_table,
+                           const void* codes, const float* scales, void* k_out, void* v_out, int B,
+                           cudaStream_t st);
+oda_status launch_qk_norm_rope(oda_ctx* ctx, const void* q, int64_t q_stride, const void* k,
+                               int64_t k_stride, const void* q_weight, const void* k_weight,
+                               float eps, const float* inv_freq, int rot, bool neighbours,
+                               const int32_t* positions, int pos_offset, int64_t n, void* q_out,
+                               int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                               cudaStream_t st);
 size_t select_scratch_bytes();
 oda_status launch_select(oda_ctx* ctx, const float* scores, const float* gain, long long n,
                          long long k, uint8_t* selected, double* net_gain, cudaStream_t st);

@@ -22,6 +22,9 @@ LIB_PATH = os.path.join(_HERE, "liboda.so")
 OK, ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS, ERR_STATE = range(8)
 BF16, F32 = 0, 1
 MAX_BATCH = 1024
+KV8_INT8, KV8_E4M3 = 1, 2  # formats of the 8-bit paged cache
+KV8_FORMATS = {"int8": KV8_INT8, "e4m3": KV8_E4M3}
+ROPE_NEIGHBOURS = 1       # oda_qk_norm_rope flag
 ATTN_INPUTS_READY = 1     # oda_local_attn / oda_full_attn_gated flag (see oda.h)
 # A step with at least this many layers runs the recall head's first layer over
 # h_prev and emb as a kernel of its own (oda.h, oda_step_run): one launch more.
@@ -37,6 +40,8 @@ EXPORTS = (
     "oda_step_graph_create", "oda_step_graph_launch", "oda_step_graph_run_io",
     "oda_step_graph_destroy", "oda_version",
     "oda_full_attn_gated_static", "oda_range_attn", "oda_select_budget",
+    "oda_kv8_layout", "oda_append_kv8", "oda_read_kv8", "oda_full_attn_kv8",
+    "oda_range_attn_kv8", "oda_qk_norm_rope",
 )
 
 
@@ -57,6 +62,11 @@ class OdaLayoutInfo(ctypes.Structure):
     _fields_ = [("tile_elems", c_int64), ("cache_layer_elems", c_int64),
                 ("ring_blocks", c_int64), ("ring_layer_elems", c_int64),
                 ("elem_bytes", c_int64)]
+
+
+class OdaKv8LayoutInfo(ctypes.Structure):
+    _fields_ = [("tile_bytes", c_int64), ("cache_layer_bytes", c_int64),
+                ("scale_layer_elems", c_int64)]
 
 
 class OdaStepDesc(ctypes.Structure):
@@ -106,6 +116,16 @@ def lib() -> ctypes.CDLL:
         "oda_range_attn": [vp, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_int,
                            ctypes.c_uint, vp],
         "oda_select_budget": [vp, vp, vp, c_int64, c_int64, vp, vp, vp],
+        "oda_kv8_layout": [POINTER(OdaConfig), POINTER(OdaKv8LayoutInfo)],
+        "oda_append_kv8": [vp, c_int, c_int, c_int, vp, vp, vp, c_int64, vp, vp, vp, vp, vp,
+                           c_int, vp],
+        "oda_read_kv8": [vp, c_int, c_int, c_int, vp, c_int64, vp, vp, vp, vp, vp, vp, c_int, vp],
+        "oda_full_attn_kv8": [vp, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_int,
+                              ctypes.c_uint, vp],
+        "oda_range_attn_kv8": [vp, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                               c_int, ctypes.c_uint, vp],
+        "oda_qk_norm_rope": [vp, vp, c_int64, vp, c_int64, vp, vp, c_float, vp, c_int, vp, c_int,
+                             c_int64, vp, c_int64, vp, c_int64, ctypes.c_uint, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -166,6 +186,29 @@ def layout(cfg: OdaConfig) -> dict:
     info = OdaLayoutInfo()
     _check(lib().oda_layout(ctypes.byref(cfg), ctypes.byref(info)), "oda_layout")
     return {k: int(getattr(info, k)) for k, _ in OdaLayoutInfo._fields_}
+
+
+def kv8_layout(cfg: OdaConfig) -> dict:
+    """Sizes of the 8-bit paged cache of a configuration (oda_kv8_layout)."""
+    info = OdaKv8LayoutInfo()
+    _check(lib().oda_kv8_layout(ctypes.byref(cfg), ctypes.byref(info)), "oda_kv8_layout")
+    return {k: int(getattr(info, k)) for k, _ in OdaKv8LayoutInfo._fields_}
+
+
+def _format(f) -> int:
+    return KV8_FORMATS.get(f, f)
+
+
+def _heads(x, d, what):
+    """(pointer, token stride) of [n][heads][d] whose heads are contiguous."""
+    if x is None:
+        return None, 0
+    if not x.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    if x.dim() != 3 or x.shape[2] != d or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d):
+        raise ValueError(f"{what} must be [n][heads][{d}] with contiguous heads")
+    # one token's stride says nothing (and may be anything): its heads' extent does
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1] * d
 
 
 class OdaGraph:
@@ -293,6 +336,96 @@ class OdaContext:
                                     ptr(count), ptr(out), ptr(lse), B,
                                     ATTN_INPUTS_READY if inputs_ready else 0, _stream(stream)),
                "oda_range_attn")
+
+    # ------------------------------------------------------ the 8-bit cache
+    # format: "int8" or "e4m3" (or KV8_INT8, KV8_E4M3)
+    def _tokens(self, x, layer_begin, layer_end, what):
+        """n_tokens of an [layers][n_tokens][hkv][d] tensor of the context's dtype."""
+        import torch
+        c = self.cfg
+        if x.dtype != (torch.bfloat16 if c.dtype == BF16 else torch.float32):
+            raise ValueError(f"{what} must have the context's dtype")
+        if x.dim() != 4 or x.shape[0] != layer_end - layer_begin or x.shape[2] != c.hkv or \
+                x.shape[3] != c.head_dim:
+            raise ValueError(f"{what} must be [layers][n_tokens][hkv][d]")
+        return x.shape[1]
+
+    def append_kv8(self, format, layer_begin, layer_end, k_new, v_new, seq_lens, block_table,
+                   codes, scales, ring, B, tok_start=None, stream=None):
+        """Quantise the rows' new tokens into the 8-bit cache, and into the ring as
+        they are (oda_append_kv8). tok_start: None for one token a row."""
+        n = self._tokens(k_new, layer_begin, layer_end, "k_new")
+        if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+            raise ValueError("k_new and v_new differ in shape or type")
+        _check(lib().oda_append_kv8(self.handle, _format(format), layer_begin, layer_end,
+                                    ptr(k_new), ptr(v_new), ptr(tok_start), n, ptr(seq_lens),
+                                    ptr(block_table), ptr(codes), ptr(scales), ptr(ring), B,
+                                    _stream(stream)), "oda_append_kv8")
+
+    def read_kv8(self, format, layer_begin, layer_end, seq_lens, block_table, codes, scales,
+                 k_out, v_out, B, tok_start=None, stream=None):
+        """The rows' positions up to seq_lens out of the 8-bit cache (oda_read_kv8);
+        k_out or v_out may be None."""
+        ns = [self._tokens(x, layer_begin, layer_end, w)
+              for x, w in ((k_out, "k_out"), (v_out, "v_out")) if x is not None]
+        if not ns or ns[0] != ns[-1]:
+            raise ValueError("read_kv8 needs k_out or v_out, of one length")
+        _check(lib().oda_read_kv8(self.handle, _format(format), layer_begin, layer_end,
+                                  ptr(tok_start), ns[0], ptr(seq_lens), ptr(block_table),
+                                  ptr(codes), ptr(scales), ptr(k_out), ptr(v_out), B,
+                                  _stream(stream)), "oda_read_kv8")
+
+    def full_attn_kv8(self, format, layer, q, seq_lens, block_table, codes, scales, idx, count,
+                      out, lse, B, stream=None, inputs_ready=False):
+        """full_attn_gated over the 8-bit cache (oda_full_attn_kv8)."""
+        _check(lib().oda_full_attn_kv8(self.handle, _format(format), layer, ptr(q), ptr(seq_lens),
+                                       ptr(block_table), ptr(codes), ptr(scales), ptr(idx),
+                                       ptr(count), ptr(out), ptr(lse), B,
+                                       ATTN_INPUTS_READY if inputs_ready else 0,
+                                       _stream(stream)), "oda_full_attn_kv8")
+
+    def range_attn_kv8(self, format, layer, q, seq_lens, range_lo, range_hi, block_table, codes,
+                       scales, idx, count, out, lse, B, stream=None, inputs_ready=False):
+        """range_attn over the 8-bit cache (oda_range_attn_kv8)."""
+        _check(lib().oda_range_attn_kv8(self.handle, _format(format), layer, ptr(q),
+                                        ptr(seq_lens), ptr(range_lo), ptr(range_hi),
+                                        ptr(block_table), ptr(codes), ptr(scales), ptr(idx),
+                                        ptr(count), ptr(out), ptr(lse), B,
+                                        ATTN_INPUTS_READY if inputs_ready else 0,
+                                        _stream(stream)), "oda_range_attn_kv8")
+
+    def qk_norm_rope(self, q, k, q_weight, k_weight, eps, inv_freq, positions, q_out, k_out,
+                     pos_offset=0, interleaved=False, stream=None):
+        """RMS norm of every head (weights may be None) and rotation by position
+        (oda_qk_norm_rope). q [n][hq][d], k [n][hkv][d] or None, with any token
+        stride; inv_freq float32 [rot_dim / 2] or None for the norm alone;
+        interleaved: pairs are neighbours instead of halves apart."""
+        import torch
+        c = self.cfg
+        d = c.head_dim
+        n = q.shape[0]
+        dt = torch.bfloat16 if c.dtype == BF16 else torch.float32
+        for x, heads in ((q, c.hq), (q_out, c.hq), (k, c.hkv), (k_out, c.hkv)):
+            if x is not None and (x.dtype != dt or x.shape[0] != n or x.shape[1] != heads):
+                raise ValueError("q and k must be [n][hq][d] and [n][hkv][d] of the context's dtype")
+        for x in (q_weight, k_weight):
+            if x is not None and (x.dtype != dt or x.numel() != d):
+                raise ValueError("a norm weight must be [d] of the context's dtype")
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            if inv_freq.dtype != torch.float32 or positions.dtype != torch.int32 or \
+                    positions.numel() != n:
+                raise ValueError("inv_freq must be float32, positions int32 [n]")
+        qp, qs = _heads(q, d, "q")
+        kp, ks = _heads(k, d, "k")
+        qo, qos = _heads(q_out, d, "q_out")
+        ko, kos = _heads(k_out, d, "k_out")
+        _check(lib().oda_qk_norm_rope(self.handle, qp, qs, kp, ks, ptr(q_weight), ptr(k_weight),
+                                      float(eps), ptr(inv_freq), rot, ptr(positions),
+                                      int(pos_offset), n, qo, qos, ko, kos,
+                                      ROPE_NEIGHBOURS if interleaved else 0, _stream(stream)),
+               "oda_qk_norm_rope")
 
     def get_device_error(self, stream=None) -> int:
         e = c_int(0)

@@ -10,6 +10,9 @@
  *      (oda_full_attn_gated),
  * plus a captured CUDA graph of the whole step whose Full part sits behind a
  * device-side conditional node (oda_step_graph_*).
+ * Beside them: the norm and rotation that make the queries and keys of a step
+ * out of the projections (oda_qk_norm_rope), and a paged cache held in 8 bits
+ * with the Full and range attention that read it (oda_*_kv8).
  *
  * Sources (web pages restated by this library):
  *   [SUM]  "On-Demand Attention (ODA)" summary, picx.dev
@@ -331,6 +334,136 @@ oda_status oda_full_attn_gated_static(const oda_config* cfg, int layer, const vo
                                       const void* kv_cache, const int32_t* idx,
                                       const int32_t* count, void* out, float* lse, int B,
                                       int32_t* err, oda_stream stream);
+
+/* ----------------------------------------------------------------------- */
+/* The 8-bit paged cache                                                     */
+/* ----------------------------------------------------------------------- */
+/*
+ * The pages fix what Full attention reads, not the type it is stored in. Held
+ * in 8 bits the history takes half the memory of bf16 and half the time to
+ * read; Local keeps reading the ring, in the context's dtype.
+ *
+ * Per layer, layers back to back (row-major, innermost last):
+ *   codes   uint8 [num_blocks][hkv][2][16][d]   as the paged cache, one byte each
+ *   scales  float [num_blocks][hkv][2]          one for each block, KV head and K or V
+ * with the context's block table. The value of an element is code * scale,
+ * where `format` says what a byte stands for:
+ *   ODA_KV8_INT8  a whole number, two's complement, within [-127, 127]; top = 127
+ *   ODA_KV8_E4M3  a float with 4 exponent and 3 mantissa bits;          top = 448
+ * Writing a block's new tokens (a = their largest |x|, per KV head and K or V):
+ *   scale = max(a / top, the block's scale so far); 0 where that is below 2^-107,
+ *   code  = x * (1 / scale) rounded to the format, ties to even,
+ * the quotients and the product rounded to float32. The "scale so far" counts
+ * while the block holds earlier tokens of the row (new tokens that start in its
+ * slot 0 start it anew). Where the scale grows, the codes held before become
+ * code * (old scale * (1 / scale)), rounded again: a token that arrives alone
+ * may be rounded up to 15 times before its block is full, tokens written
+ * together once. A value that is not finite makes its block's scale NaN, and
+ * the whole block (of that head, K or V) reads back as NaN until it is started
+ * anew.
+ * Pointers to codes must be 16-byte aligned, to scales 8-byte aligned.
+ *
+ * Errors: an unknown format is ODA_ERR_DTYPE; calling with another device current
+ * than the context's, ODA_ERR_STATE; a null or misaligned pointer ODA_ERR_ARG.
+ */
+#define ODA_KV8_INT8 1
+#define ODA_KV8_E4M3 2
+
+typedef struct oda_kv8_layout_info {
+  int64_t tile_bytes;          /* codes of one (block, kv_head): [2][16][d]            */
+  int64_t cache_layer_bytes;   /* codes, one layer: [num_blocks][hkv][2][16][d]        */
+  int64_t scale_layer_elems;   /* scales (float), one layer: [num_blocks][hkv][2]      */
+} oda_kv8_layout_info;
+
+/* Sizes of the 8-bit cache of a configuration. Host only; errors as oda_layout. */
+oda_status oda_kv8_layout(const oda_config* cfg, oda_kv8_layout_info* out);
+
+/*
+ * Quantise the rows' new tokens into the 8-bit cache, for layers [layer_begin,
+ * layer_end) in one launch: one token a row (a decode step) or any number (a
+ * prefill chunk), also across block borders.
+ *   tok_start   device int32 [B+1], ascending from 0 to n_tokens: row b's new tokens
+ *               are k_new[l][tok_start[b] .. tok_start[b+1]); a row may have none.
+ *               NULL: one token per row, n_tokens = B.
+ *   k_new, v_new  device, [layer_end-layer_begin][n_tokens][hkv][d], context dtype
+ *   seq_lens    device int32 [B], position of the row's last new token: the n
+ *               tokens are positions seq_lens[b]-n+1 .. seq_lens[b]
+ *   codes, scales  the 8-bit cache of ALL layers (layer 0 base)
+ *   ring        ring of ALL layers in the context dtype, or NULL: receives what
+ *               oda_append_kv would have written for these positions
+ * Slots behind a row's last position keep what they hold. A row with n > 0 and
+ * seq_lens[b] < n, a tok_start that is not ascending within [0, n_tokens], or a
+ * block out of range records ODA_ERR_BOUNDS and that row or block is skipped.
+ * No physical block may be written through two (row, column) pairs in one call:
+ * its contents are then unspecified. n_tokens <= 2^31 - 1.
+ */
+oda_status oda_append_kv8(oda_ctx* ctx, int format, int layer_begin, int layer_end,
+                          const void* k_new, const void* v_new, const int32_t* tok_start,
+                          int64_t n_tokens, const int32_t* seq_lens, const int32_t* block_table,
+                          void* codes, float* scales, void* ring, int B, oda_stream stream);
+
+/*
+ * Read positions back out of the 8-bit cache, as code * scale rounded once to
+ * the context dtype. The arguments mirror oda_append_kv8: row b's positions
+ * seq_lens[b]-n+1 .. seq_lens[b] (n from tok_start; one if NULL) go to
+ * k_out[l][tok_start[b] ..], v_out likewise ([layers][n_tokens][hkv][d]; either
+ * may be NULL). Tokens of a row or block with an error stay as they were.
+ */
+oda_status oda_read_kv8(oda_ctx* ctx, int format, int layer_begin, int layer_end,
+                        const int32_t* tok_start, int64_t n_tokens, const int32_t* seq_lens,
+                        const int32_t* block_table, const void* codes, const float* scales,
+                        void* k_out, void* v_out, int B, oda_stream stream);
+
+/*
+ * oda_full_attn_gated and oda_range_attn over the 8-bit cache: the same rows,
+ * regions, layouts, outputs and errors, K and V being code * scale. The scales
+ * are applied to scores and weights in float32; queries and weights go through
+ * the tensor cores with at least 22 bits, so the result is that of float32
+ * arithmetic on the stored values. flags: 0 or ODA_ATTN_INPUTS_READY, which then
+ * covers codes and scales. Slots of a block outside the row's positions or the
+ * region may hold anything.
+ */
+oda_status oda_full_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
+                             const int32_t* seq_lens, const int32_t* block_table,
+                             const void* codes, const float* scales, const int32_t* idx,
+                             const int32_t* count, void* out, float* lse, int B, unsigned flags,
+                             oda_stream stream);
+oda_status oda_range_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
+                              const int32_t* seq_lens, const int32_t* range_lo,
+                              const int32_t* range_hi, const int32_t* block_table,
+                              const void* codes, const float* scales, const int32_t* idx,
+                              const int32_t* count, void* out, float* lse, int B, unsigned flags,
+                              oda_stream stream);
+
+/*
+ * What makes a step's queries and keys ready for the cache and the attention
+ * (which take them as already rotated): the RMS norm of every head and the
+ * rotation by position, one launch for n tokens. For each head x of a token:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (as it is where weight is NULL),
+ *   pair i of the first rot_dim elements turns by
+ *   (positions[token] + pos_offset) * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin);
+ * the other elements stay y. Float32 throughout, the angle reduced from
+ * float64, one rounding at the end.
+ *   q, q_out  device [n][hq][d], k, k_out device [n][hkv][d] (k NULL: queries only),
+ *             context dtype; *_stride: elements from one token to the next (the
+ *             heads of a token are contiguous), a multiple of 16 bytes, so q
+ *             and k may be views of one projection's output. An output may be its
+ *             input (same pointer and stride); any other overlap is not allowed.
+ *   q_weight, k_weight  device [d], context dtype, or NULL
+ *   inv_freq  device float [rot_dim / 2]; rot_dim a multiple of 16 within [0, d]
+ *             (0: the norm alone; inv_freq and positions may be NULL)
+ *   positions device int32 [n]
+ *   flags     0: pair i is (i, i + rot_dim / 2); ODA_ROPE_NEIGHBOURS: (2i, 2i + 1)
+ * 0 <= n <= 2^31 - 1; eps >= 0. Pointers 16-byte aligned (positions, inv_freq: 4).
+ */
+#define ODA_ROPE_NEIGHBOURS 1u
+oda_status oda_qk_norm_rope(oda_ctx* ctx, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* q_weight, const void* k_weight,
+                            float eps, const float* inv_freq, int rot_dim,
+                            const int32_t* positions, int pos_offset, int64_t n, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            unsigned flags, oda_stream stream);
 
 /* Synchronize `stream`, then return and clear the sticky device error word
  * (ODA_OK if none). Call outside the hot loop. */

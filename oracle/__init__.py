@@ -18,3 +18,4 @@ Parity status per function is listed in ``oracle/oda_oracle.py``'s header.
 """
 
 from .oda_oracle import *  # noqa: F401,F403
+from .kv8_oracle import *  # noqa: F401,F403

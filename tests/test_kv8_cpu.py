@@ -1,0 +1,176 @@
+"""The 8-bit cache on the CPU: the oracle's own pins, the sizes and refusals
+that need no GPU, and the numbering of the write's work items."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle as O
+from tests.test_boundary import _cfg, _ensure_built
+
+
+# ------------------------------------------------------------------ the oracle
+
+def test_e4m3_bytes_round_trip():
+    b = np.arange(256, dtype=np.uint8)
+    v = O.kv8_value(b, "e4m3")
+    fine = ~np.isnan(v)
+    assert fine.sum() == 254
+    n, byte = O.kv8_round(v[fine], "e4m3")
+    assert np.array_equal(n, v[fine]) and np.array_equal(byte, b[fine])
+    assert v[0x7e] == 448 and v[1] == 2.0 ** -9 and v[0x38] == 1.0
+
+
+def test_rounding_is_to_nearest_with_ties_to_even():
+    grid = np.unique(O.kv8_value(np.arange(127, dtype=np.uint8), "e4m3"))
+    mid = (grid[1:] + grid[:-1]) / 2
+    got = O.kv8_round(mid, "e4m3")[1]
+    assert np.all(got % 2 == 0)                            # the even neighbour
+    y = np.random.default_rng(1).uniform(-500, 500, 4000)
+    n, _ = O.kv8_round(y, "e4m3")
+    near = grid[np.abs(np.abs(y)[:, None] - grid).argmin(1)]
+    assert np.array_equal(np.abs(n), near)
+    assert np.array_equal(O.kv8_round([0.5, 1.5, -2.5, 127.4, 300], "int8")[0], [0, 2, -2, 127, 127])
+
+
+def test_oracle_matches_torch_rounding():
+    torch = pytest.importorskip("torch")
+    y = torch.randn(20000, generator=torch.Generator().manual_seed(3)) * 60
+    want = y.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(O.kv8_round(y.numpy().astype(np.float64), "e4m3")[1], want)
+
+
+@pytest.mark.parametrize("fmt,step", [("int8", 0.5 / 127), ("e4m3", 2.0 ** -4)])
+def test_a_block_written_at_once_and_token_by_token(fmt, step):
+    """At once every element is within half a step of the format; token by token
+    each growth of the scale may add half a step of the scale it grew to."""
+    r = np.random.default_rng(5)
+    x = r.standard_normal((16, 64)).astype(np.float32).astype(np.float64)
+    one = np.zeros((16, 64), np.uint8)
+    s1 = O.kv8_write_block(one, 0.0, 0, x, fmt)
+    top = np.abs(x).max()
+    e = np.abs(O.kv8_value(one, fmt) * s1 - x)
+    unit = np.full_like(x, top) if fmt == "int8" else np.maximum(np.abs(x), top * 2.0 ** -14)
+    assert np.all(e <= step * unit * (1 + 1e-6))
+    many, s, scales = np.zeros((16, 64), np.uint8), 0.0, []
+    for i in range(16):
+        s = O.kv8_write_block(many, s, i, x[i:i + 1], fmt)
+        scales.append(s)
+    assert s == s1 and sorted(scales) == scales
+    growths = len(set(scales)) + 1
+    e = np.abs(O.kv8_value(many, fmt) * s - x)
+    assert np.all(e <= growths * step * unit * (1 + 1e-6))
+
+
+def test_zero_tiny_and_infinite_blocks():
+    c = np.full((16, 64), 7, np.uint8)
+    assert O.kv8_write_block(c, 0.0, 0, np.zeros((16, 64)), "int8") == 0.0 and not c.any()
+    assert O.kv8_write_block(c, 0.0, 0, np.full((16, 64), 2.0 ** -101), "e4m3") == 0.0
+    x = np.ones((3, 64))
+    x[1, 5] = np.inf
+    assert np.isnan(O.kv8_write_block(c, 0.0, 0, x, "int8"))
+    assert np.isnan(O.kv8_write_block(c, np.nan, 3, np.ones((1, 64)), "int8"))
+    assert O.kv8_write_block(c, np.nan, 0, np.ones((1, 64)), "int8") == np.float32(1 / 127)
+
+
+def test_norm_rotate_special_cases():
+    r = np.random.default_rng(2)
+    x = r.standard_normal((3, 2, 8))
+    f = 1.0 / 10.0 ** np.arange(3)
+    for nb in (False, True):
+        y = O.norm_rotate(x, None, 0.0, [0, 0, 0], f, nb)
+        assert np.array_equal(y, x)                        # position 0 turns nothing
+        y = O.norm_rotate(x, None, 0.0, [5, 9, 2 ** 20], f, nb)
+        assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1))
+        assert np.array_equal(y[..., 6:], x[..., 6:])      # behind the rotated part
+    # the score of a rotated pair depends on the distance of their positions only
+    q, k = r.standard_normal((1, 1, 8)), r.standard_normal((1, 1, 8))
+    a = [(O.norm_rotate(q, None, 0, [p], f) * O.norm_rotate(k, None, 0, [p - 3], f)).sum() for p in (3, 500)]
+    assert abs(a[0] - a[1]) < 1e-12
+    y = O.norm_rotate(3.0 * x, np.ones(8), 0.0, [0] * 3, f)
+    assert np.allclose((y ** 2).mean(-1), 1.0)
+
+
+# ------------------------------------------------------------ sizes, refusals
+
+def test_kv8_layout():
+    _ensure_built()
+    from gated_local_full_b200 import oda
+    lay = oda.kv8_layout(_cfg())
+    assert lay == dict(tile_bytes=2 * 16 * 128, cache_layer_bytes=8257 * 8 * 4096,
+                       scale_layer_elems=8257 * 8 * 2)
+    assert oda.kv8_layout(_cfg(head_dim=64, dtype="f32"))["tile_bytes"] == 2048
+    with pytest.raises(oda.OdaError) as e:
+        oda.kv8_layout(_cfg(head_dim=96))
+    assert e.value.status == oda.ERR_SHAPE
+
+
+def test_null_contexts_are_refused():
+    _ensure_built()
+    from gated_local_full_b200 import oda
+    L = oda.lib()
+    n = None
+    assert L.oda_kv8_layout(n, n) == oda.ERR_ARG
+    assert L.oda_append_kv8(n, 1, 0, 1, n, n, n, 1, n, n, n, n, n, 1, n) == oda.ERR_ARG
+    assert L.oda_read_kv8(n, 1, 0, 1, n, 1, n, n, n, n, n, n, 1, n) == oda.ERR_ARG
+    assert L.oda_full_attn_kv8(n, 1, 0, n, n, n, n, n, n, n, n, n, 1, 0, n) == oda.ERR_ARG
+    assert L.oda_range_attn_kv8(n, 1, 0, n, n, n, n, n, n, n, n, n, n, n, 1, 0, n) == oda.ERR_ARG
+    assert L.oda_qk_norm_rope(n, n, 0, n, 0, n, n, 1e-6, n, 0, n, 0, 1, n, 0, n, 0, 0, n) == oda.ERR_ARG
+
+
+def test_tensors_off_the_gpu_are_refused():
+    torch = pytest.importorskip("torch")
+    _ensure_built()
+    from gated_local_full_b200 import oda
+
+    class Ctx(oda.OdaContext):                             # the binding's checks alone
+        def __init__(self, cfg):
+            self.cfg, self.handle = cfg, None
+
+    ctx = Ctx(_cfg())
+    kv = torch.zeros((1, 2, 8, 128), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        ctx.append_kv8("int8", 0, 1, kv, kv, i, i, kv, kv, None, 2)
+    with pytest.raises(ValueError, match="dtype"):
+        ctx.append_kv8("int8", 0, 1, kv.float(), kv.float(), i, i, kv, kv, None, 2)
+    with pytest.raises(ValueError, match="layers"):
+        ctx.append_kv8("int8", 0, 2, kv, kv, i, i, kv, kv, None, 2)
+    with pytest.raises(ValueError, match="differ"):
+        ctx.append_kv8("int8", 0, 1, kv, kv[:, :1], i, i, kv, kv, None, 2)
+    with pytest.raises(ValueError, match="needs"):
+        ctx.read_kv8("int8", 0, 1, i, i, kv, kv, None, None, 2)
+    q, k = torch.zeros((2, 16, 128), dtype=torch.bfloat16), torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    f = torch.ones(64)
+    with pytest.raises(ValueError, match="context's dtype"):
+        ctx.qk_norm_rope(q.float(), k, None, None, 0.0, f, i, q, k)
+    with pytest.raises(ValueError, match="context's dtype"):
+        ctx.qk_norm_rope(q, k[:, :4], None, None, 0.0, f, i, q, k)
+    with pytest.raises(ValueError, match="positions"):
+        ctx.qk_norm_rope(q, k, None, None, 0.0, f, i.long(), q, k)
+    with pytest.raises(ValueError, match="norm weight"):
+        ctx.qk_norm_rope(q, k, f.bfloat16(), None, 0.0, f, i, q, k)
+    with pytest.raises(ValueError, match="GPU"):
+        ctx.qk_norm_rope(q, k, None, None, 0.0, f, i, q, k)
+
+
+def test_write_items_never_meet():
+    """Row b's items start at tok_start[b] // 16 + 2 b; a row of n tokens touches
+    at most n // 16 + 2 blocks, wherever its first token falls."""
+    r = np.random.default_rng(9)
+    for _ in range(300):
+        B = int(r.integers(1, 12))
+        n = r.integers(0, 70, B) * r.integers(0, 2, B)
+        past = r.integers(0, 100, B)
+        ts = np.concatenate([[0], np.cumsum(n)])
+        items, used = int(ts[-1]) // 16 + 2 * B, set()
+        start = [int(ts[b]) // 16 + 2 * b for b in range(B)]
+        for b in range(B):
+            if n[b]:
+                touched = (past[b] + n[b] - 1) // 16 - past[b] // 16 + 1
+                for j in range(touched):
+                    it = start[b] + j
+                    assert it < items and it not in used
+                    assert max(x for x in range(B) if start[x] <= it) == b
+                    used.add(it)
