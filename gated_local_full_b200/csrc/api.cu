@@ -72,6 +72,7 @@ oda_status attn_kv8(oda_ctx* ctx, int format, int layer, const void* q, const in
     return ODA_ERR_ARG;
   return oda_impl::launch_attn_kv8(ctx, format, layer, q, seq_lens, range_lo, range_hi,
                                    block_table, codes, scales, idx, count, out, lse, B,
+                                   (flags & ODA_ATTN_INPUTS_READY) != 0,
                                    static_cast<cudaStream_t>(stream));
 }
 

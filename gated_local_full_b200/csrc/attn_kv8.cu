@@ -34,12 +34,14 @@
 //     product: probabilities never leave their lane.
 #include "kv8.cuh"
 #include "plan.cuh"
+#include "tiles.cuh"
 
 using namespace oda;
 
 namespace {
 
 constexpr int W = 8;                     // warps per CTA
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per barrier wait
 
 struct Attn8Args {
   const void* q;
@@ -54,7 +56,8 @@ struct Attn8Args {
   const int32_t* range_lo;
   const int32_t* range_hi;
   long long num_blocks;
-  int max_blocks, B, hkv, G, max_batch;
+  int max_blocks, B, hkv, G, max_batch, ns;
+  int early;                             // stage the first tiles before the dependency wait
   float qscale;                          // log2(e) / sqrt(d)
   float* partials;                       // [max_parts][G][d], then [max_parts][G][2]
   int max_parts;
@@ -68,6 +71,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 bytes from global to shared memory whose arrival counts on a barrier.
+__device__ __forceinline__ void cp_async8_arrive(uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile(
+      "cp.async.ca.shared.global [%0], [%1], 8;\n\t"
+      "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(dst), "l"(src), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -286,20 +297,111 @@ struct State {
   }
 };
 
-// Bits [lo, hi) of a 16-bit tile mask whose bit 0 is slot `base`.
-__device__ __forceinline__ uint32_t slots(int lo, int hi, int base) {
-  const int l = min(max(lo - base, 0), 16);
-  const int h = min(max(hi - base, 0), 16);
-  return h <= l ? 0u : (((1u << h) - 1u) & ~((1u << l) - 1u));
+// Shared memory of a launch, in order.
+struct Smem {
+  size_t wstate, rows, bars, scale, tile, bad, total;
+  __host__ __device__ Smem(int G, int d, int max_batch, int ns) {
+    const size_t state = (size_t)W * G * (d + 4) * 4, merge = (size_t)W * 32 * 6 * 4;
+    size_t at = (size_t)W * ns * 2 * ODA_TILE * d;           // stages
+    wstate = at;                                             // [W][G][d + 4], or the merge's
+    at += state > merge ? state : merge;
+    bars = at;                                               // [W][ns]
+    at += (size_t)W * ns * 8;
+    scale = at;                                              // [W][ns] float2
+    at += (size_t)W * ns * 8;
+    tile = at;                                               // [W][ns] tile of each stage
+    at += (size_t)W * ns * 4;
+    bad = at;                                                // [W][ns] its block is out of range
+    at += (size_t)W * ns * 4;
+    rows = at;                                               // 5 arrays by row slot
+    at += (size_t)(5 * max_batch + 2) * 4;
+    total = (at + 15) & ~(size_t)15;
+  }
+};
+
+// The last CTA of a segment puts its parts together. A thread takes four
+// output elements and every SPLIT-th part, U of them in one round trip.
+template <typename T, int D>
+__device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b, int g, int pbase,
+                                            int nparts) {
+  constexpr int U = 10;
+  const int tid = threadIdx.x, G = a.G;
+  const int nch = G * D / 4;                                 // 16 .. 128 chunks
+  const int split = W * 32 / nch;
+  const int ch = tid % nch, part = tid / nch;
+  const int h = ch * 4 / D;
+  const float* pml = a.partials + (size_t)a.max_parts * G * D;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = part; j0 < nparts; j0 += U * split) {
+    float2 ml[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * split;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < nparts) {
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(pml) + (long long)(pbase + j) * G + h);
+        v[u] = __ldcg(reinterpret_cast<const float4*>(a.partials + (long long)(pbase + j) * G * D) + ch);
+      }
+    }
+    float mt = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mt = fmaxf(mt, ml[u].x);
+    if (l != 0.f) {
+      const float f = fast_exp2(m - mt);
+      l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].y == 0.f) continue;                          // no token (a NaN is not left out)
+      const float f = fast_exp2(ml[u].x - mt);
+      l = fmaf(ml[u].y, f, l);
+      acc.x = fmaf(v[u].x, f, acc.x); acc.y = fmaf(v[u].y, f, acc.y);
+      acc.z = fmaf(v[u].z, f, acc.z); acc.w = fmaf(v[u].w, f, acc.w);
+    }
+    m = mt;
+  }
+  // the threads of one chunk, through shared memory: [6][W * 32]
+  float* s = sm + tid;
+  s[0] = m; s[W * 32] = l;
+  s[2 * W * 32] = acc.x; s[3 * W * 32] = acc.y; s[4 * W * 32] = acc.z; s[5 * W * 32] = acc.w;
+  __syncthreads();
+  if (part == 0) {
+    float mt = m;
+    for (int p = 1; p < split; ++p) mt = fmaxf(mt, sm[p * nch + ch]);
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < split; ++p) {
+      const float* x = sm + p * nch + ch;
+      if (x[W * 32] == 0.f) continue;
+      const float f = fast_exp2(x[0] - mt);
+      l += x[W * 32] * f;
+      acc.x += x[2 * W * 32] * f; acc.y += x[3 * W * 32] * f;
+      acc.z += x[4 * W * 32] * f; acc.w += x[5 * W * 32] * f;
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const long long head = (long long)b * a.hkv * G + g * G + h;
+    T* o = static_cast<T*>(a.out) + head * D + ch * 4 % D;
+    o[0] = (T)(acc.x * inv); o[1] = (T)(acc.y * inv); o[2] = (T)(acc.z * inv); o[3] = (T)(acc.w * inv);
+    if (ch * 4 % D == 0 && a.lse)
+      a.lse[head] = l != 0.f ? (mt + fast_log2(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
+// A persistent grid takes the tiles as plan.cuh divides them; a CTA's share
+// may lie in one segment (row, KV head) or span several. Each warp streams
+// its own tiles, every W-th of the share, through a.ns stages of shared memory
+// with bulk copies, and runs ahead of its arithmetic across segments.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) {
   constexpr int TILE = 2 * ODA_TILE * D;
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int G = a.G;
-  float* wstate = reinterpret_cast<float*>(smem);                      // [W][G][D + 4]
-  int* rowstart = reinterpret_cast<int*>(wstate + W * G * (D + 4));    // [max_batch + 1]
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int G = a.G, ns = a.ns;
+  const Smem lay(G, D, a.max_batch, ns);
+  float* wstate = reinterpret_cast<float*>(smem + lay.wstate);
+  int* rowstart = reinterpret_cast<int*>(smem + lay.rows);             // [max_batch + 1]
   int* rowcs = rowstart + a.max_batch + 1;                             // [max_batch + 1]
   int* rowb = rowcs + a.max_batch + 1;                                 // [max_batch] each
   int* rowt = rowb + a.max_batch;
@@ -307,8 +409,17 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   __shared__ int sinfo[9];
   __shared__ int slast;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_launch_dependents();
+  unsigned char* stages = smem + (size_t)warp * ns * TILE;
+  const uint32_t bars = smem_addr(smem + lay.bars + (size_t)warp * ns * 8);
+  float2* sscale = reinterpret_cast<float2*>(smem + lay.scale) + warp * ns;
+  int* stile = reinterpret_cast<int*>(smem + lay.tile) + warp * ns;
+  int* sbad = reinterpret_cast<int*>(smem + lay.bad) + warp * ns;
+  if (lane < ns) mbar_init(bars + 8 * lane, 2);    // the codes' bytes, the scales
+  fence_mbar_init();
+  if (!a.early) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   if (warp == 0) {
     PlanIn p = {};
     p.B = a.B;
@@ -334,47 +445,110 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   __syncthreads();
   const int nr = sinfo[0], total = sinfo[1], P = sinfo[2], aligned = sinfo[3];
   const int lo = sinfo[4], hi = sinfo[5];
-  if (nr <= 0 || total <= 0 || lo >= hi) return;
-  const int hq = a.hkv * G;
+  const bool work = nr > 0 && total > 0 && lo < hi;
+  if (!work) {
+    if (a.early) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
+    return;
+  }
+  const uint64_t policy = l2_policy_evict_first();           // K/V is read once a launch
+
+  // ---- producer: the tiles of this warp, in order
+  Cursor prod;
+  prod.k = lo;
+  locate(rowstart, nr, a.hkv, lo, prod);
+  prod.k = min(lo + warp, hi);
+  normalize(rowstart, a.hkv, hi, warp, prod);
+  int bc_row = -1, bc_base = 0, bc_val = -1;                 // blocks of its next 32 tiles, one a lane
+  int pstage = 0, cstage = 0, flying = 0;
+  uint32_t parity = 0;
+  auto issue = [&]() {                                       // the next tile into stage pstage
+    const int jt = prod.k - (rowstart[prod.i] + prod.g * prod.nt);
+    if (prod.i != bc_row || jt < bc_base || jt >= bc_base + 32 * W || (jt - bc_base) % W != 0) {
+      bc_row = prod.i;
+      bc_base = jt;
+      const int jl = jt + lane * W;
+      bc_val = jl < prod.nt ? a.block_table[(long long)rowb[prod.i] * a.max_blocks +
+                                            (rowlo[prod.i] - 1) / ODA_TILE + jl]
+                            : -1;
+    }
+    const int blk = __shfl_sync(0xffffffffu, bc_val, (jt - bc_base) / W);
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * pstage;
+      const bool bad = blk < 0 || (long long)blk >= a.num_blocks;
+      stile[pstage] = prod.k;
+      sbad[pstage] = bad;
+      if (bad) {
+        record_error(a.err, ODA_ERR_BOUNDS);
+        mbar_arrive(bar);
+        mbar_arrive(bar);
+      } else {
+        const long long th = (long long)blk * a.hkv + prod.g;
+        mbar_arrive_expect_tx(bar, TILE);
+        bulk_g2s(smem_addr(stages + (size_t)pstage * TILE), a.codes + th * TILE, TILE, bar, policy);
+        cp_async8_arrive(smem_addr(sscale + pstage), a.scales + th * 2, bar);
+      }
+    }
+    pstage = pstage + 1 == ns ? 0 : pstage + 1;
+    ++flying;
+    prod.k += W;
+    normalize(rowstart, a.hkv, hi, warp, prod);
+  };
+  for (int s = 0; s < ns && prod.k < hi; ++s) issue();
+  if (a.early) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   float* pacc = a.partials;
   float* pml = a.partials + (size_t)a.max_parts * G * D;
-  // row of tile lo
-  int i = 0;
-  {
-    int x = 0, y = nr - 1;
-    while (x < y) {
-      const int mid = (x + y + 1) >> 1;
-      if (rowstart[mid] <= lo) x = mid; else y = mid - 1;
-    }
-    i = x;
-  }
-  int nt = (rowstart[i + 1] - rowstart[i]) / a.hkv;
-  int g = (lo - rowstart[i]) / nt;
-  int s0 = rowstart[i] + g * nt;                       // the segment's first tile
-  for (int k0 = lo; k0 < hi;) {
-    const int s1 = s0 + nt, k1 = min(s1, hi);
-    const int b = rowb[i];
-    const int first = rowlo[i], last = rowt[i];
-    const int col0 = (first - 1) / ODA_TILE;
-    const int plo = first - 1 - col0 * ODA_TILE, phi = last - col0 * ODA_TILE;
+  const int hq = a.hkv * G;
+  bool aborted = false;
+  __syncwarp();
+
+  // ---- segments of this CTA's share
+  Cursor seg;
+  seg.k = lo;
+  locate(rowstart, nr, a.hkv, lo, seg);
+  while (true) {
+    const int b = rowb[seg.i], g = seg.g;
+    const int s0 = seg.s1 - seg.nt, s1 = seg.s1;
+    const int first = rowlo[seg.i], last = rowt[seg.i];
+    const int base = (first - 1) / ODA_TILE * ODA_TILE;
+    const int plo = first - 1 - base, phi = last - base;
     State<T, D, FMT> st;
     st.reset();
     st.load_q(static_cast<const T*>(a.q) + ((long long)b * hq + g * G) * D, G, a.qscale, lane);
-    for (int k = k0 + warp; k < k1; k += W) {
-      const int jt = k - s0;
-      const int blk = a.block_table[(long long)b * a.max_blocks + col0 + jt];
-      if (blk < 0 || (long long)blk >= a.num_blocks) {
-        if (lane == 0) record_error(a.err, ODA_ERR_BOUNDS);
-        continue;
+    while (flying > 0) {
+      const int k = stile[cstage];
+      if (k >= s1) break;                                    // of a later segment
+      if (!aborted) {
+        const bool ok = __all_sync(0xffffffffu,
+                                   mbar_wait_bounded(bars + 8 * cstage, parity, kWaitLimitNs));
+        if (!ok) {
+          aborted = true;
+          if (lane == 0) record_error(a.err, ODA_ERR_TIMEOUT);
+        }
       }
-      const float2 sc = *reinterpret_cast<const float2*>(a.scales + ((long long)blk * a.hkv + g) * 2);
+      if (aborted) break;
+      const float2 sc = sscale[cstage];
+      const uint32_t mask = sbad[cstage] ? 0u : range_bits(plo, phi, (k - s0) * ODA_TILE);
       Tile<D> t;
-      load_tile<D>(t, a.codes + ((long long)blk * a.hkv + g) * TILE, lane);
-      st.tile(t, slots(plo, phi, jt * ODA_TILE), sc.x, sc.y, lane);
+      load_tile<D>(t, stages + (size_t)cstage * TILE, lane);
+      __syncwarp();                                          // every lane has its share
+      if (++cstage == ns) {
+        cstage = 0;
+        parity ^= 1u;
+      }
+      --flying;
+      if (prod.k < hi) issue();
+      if (mask) st.tile(t, mask, sc.x, sc.y, lane);
+      __syncwarp();                                          // stile, sbad of the tile just issued
     }
     st.store(wstate + warp * G * (D + 4), G, lane);
     __syncthreads();
-    const int sigma = i * a.hkv + g;
+    const int sigma = seg.i * a.hkv + g;
     int pbase, nparts, mypart;
     if (aligned) {
       pbase = sinfo[6];
@@ -387,12 +561,13 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       nparts = c_last - c_first + 1;
       mypart = (int)blockIdx.x + sigma;
     }
-    T* outp = static_cast<T*>(a.out);
     for (int o = tid; o < G * D; o += W * 32) {
       const int h = o / D, dd = o % D;
       float mt = -INFINITY;
+#pragma unroll
       for (int w = 0; w < W; ++w) mt = fmaxf(mt, wstate[(w * G + h) * (D + 4) + D + 1]);
       float lt = 0.f, at = 0.f;
+#pragma unroll
       for (int w = 0; w < W; ++w) {
         const float* ws = wstate + (w * G + h) * (D + 4);
         if (ws[D + 2] == 0.f) continue;                // no token (a NaN is not left out)
@@ -400,7 +575,8 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         at += ws[dd] * fast_exp2(ws[D] - 14.f - mt);   // M = -inf: 0, or the NaN of a NaN scale
       }
       if (nparts == 1) {
-        outp[((long long)b * hq + g * G + h) * D + dd] = (T)(lt != 0.f ? at / lt : 0.f);
+        static_cast<T*>(a.out)[((long long)b * hq + g * G + h) * D + dd] =
+            (T)(lt != 0.f ? at / lt : 0.f);
         if (dd == 0 && a.lse)
           a.lse[(long long)b * hq + g * G + h] =
               lt != 0.f ? (mt + fast_log2(lt)) * 0.69314718055994531f : -INFINITY;
@@ -415,43 +591,43 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       if (tid == 0) slast = ticket_add(&a.tickets[sigma], 1) == nparts - 1;
       __syncthreads();
       if (slast) {
-        for (int o = tid; o < G * D; o += W * 32) {
-          const int h = o / D, dd = o % D;
-          float mt = -INFINITY;
-          for (int j = 0; j < nparts; ++j)
-            mt = fmaxf(mt, __ldcg(pml + ((long long)(pbase + j) * G + h) * 2));
-          float lt = 0.f, at = 0.f;
-          for (int j = 0; j < nparts; ++j) {
-            const long long px = (long long)(pbase + j) * G + h;
-            const float pl = __ldcg(pml + px * 2 + 1);
-            if (pl == 0.f) continue;
-            const float f = fast_exp2(__ldcg(pml + px * 2) - mt);
-            lt += pl * f;
-            at += __ldcg(pacc + px * D + dd) * f;
-          }
-          outp[((long long)b * hq + g * G + h) * D + dd] = (T)(lt != 0.f ? at / lt : 0.f);
-          if (dd == 0 && a.lse)
-            a.lse[(long long)b * hq + g * G + h] =
-                lt != 0.f ? (mt + fast_log2(lt)) * 0.69314718055994531f : -INFINITY;
-        }
+        merge_parts<T, D>(a, wstate, b, g, pbase, nparts);
         if (tid == 0) a.tickets[sigma] = 0;
       }
     }
     __syncthreads();
-    k0 = k1;
-    if (k0 >= hi) break;
-    s0 = s1;                                           // the next segment with tiles
-    if (++g == a.hkv) {
-      g = 0;
-      do ++i; while (i + 1 < nr && rowstart[i + 1] == rowstart[i]);
-      nt = (rowstart[i + 1] - rowstart[i]) / a.hkv;
+    if (s1 >= hi) break;
+    // the next segment with tiles
+    do {
+      if (++seg.g == a.hkv) {
+        seg.g = 0;
+        ++seg.i;
+        seg.nt = (rowstart[seg.i + 1] - rowstart[seg.i]) / a.hkv;
+      }
+    } while (seg.nt == 0);
+    seg.s1 = s1 + seg.nt;
+  }
+  // never leave a copy landing in shared memory after exit (after a timeout
+  // the copies still flying are waited for once more, within the limit)
+  while (flying > 0) {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + 8 * cstage, parity, kWaitLimitNs))) break;
+    if (++cstage == ns) {
+      cstage = 0;
+      parity ^= 1u;
     }
+    --flying;
   }
 }
 
-size_t smem_bytes(const oda_config& c) {
+// Stages per warp: three where two CTAs of them fit an SM beside the row
+// arrays of a large batch, else two.
+int stages_for(const oda_config& c) {
   const int G = c.hq / c.hkv;
-  return (size_t)W * G * (c.head_dim + 4) * 4 + (size_t)(5 * c.max_batch + 2) * 4;
+  return Smem(G, c.head_dim, c.max_batch, 3).total <= 112 * 1024 ? 3 : 2;
+}
+
+size_t smem_bytes(const oda_config& c) {
+  return Smem(c.hq / c.hkv, c.head_dim, c.max_batch, stages_for(c)).total;
 }
 
 template <typename F>
@@ -512,7 +688,7 @@ oda_status launch_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
                            const int32_t* seq_lens, const int32_t* range_lo,
                            const int32_t* range_hi, const int32_t* block_table, const void* codes,
                            const float* scales, const int32_t* idx, const int32_t* count, void* out,
-                           float* lse, int B, cudaStream_t st) {
+                           float* lse, int B, bool early, cudaStream_t st) {
   const oda_config& c = ctx->cfg;
   Attn8Args a;
   a.q = q;
@@ -532,6 +708,8 @@ oda_status launch_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
   a.hkv = c.hkv;
   a.G = c.hq / c.hkv;
   a.max_batch = c.max_batch;
+  a.ns = stages_for(c);
+  a.early = early ? 1 : 0;
   a.qscale = 1.4426950408889634f / sqrtf((float)c.head_dim);
   a.partials = ctx->partials;
   a.max_parts = ctx->max_parts;

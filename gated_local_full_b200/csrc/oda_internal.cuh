@@ -280,7 +280,7 @@ oda_status launch_attn_kv8(oda_ctx* ctx, int format, int layer, const void* q,
                            const int32_t* seq_lens, const int32_t* range_lo,
                            const int32_t* range_hi, const int32_t* block_table, const void* codes,
                            const float* scales, const int32_t* idx, const int32_t* count, void* out,
-                           float* lse, int B, cudaStream_t st);
+                           float* lse, int B, bool early, cudaStream_t st);
 oda_status launch_append_kv8(oda_ctx* ctx, int format, int lb, int le, const void* k_new,
                              const void* v_new, const int32_t* tok_start, long long n_tokens,
                              const int32_t* seq_lens, const int32_t* block_table, void* codes,
