@@ -10,9 +10,13 @@
 // fraction of a turn goes to float32 (error below 2^-25 turns plus the
 // float64 product's, 2^-53 of the turns).
 //
-// A block takes TOK tokens. Its threads first work out each token's cosines
-// and sines once, into shared memory, for all the token's heads; then groups
-// of lanes with 16 bytes each take the heads in turn.
+// The pass is bound by HBM: every element is read once and written once. Each
+// lane owns both elements of its pairs (two 16-byte chunks half a rotated part
+// apart), so the rotation needs no exchange and the norm's sum is one
+// butterfly over the D / 16 lanes (bf16) of a head. A block takes `tok` tokens:
+// its loads are issued first, kItems heads a lane, and the tokens' cosines and
+// sines are worked out once, into shared memory, for all their heads while the
+// loads fly.
 #include "oda_internal.cuh"
 
 using namespace oda;
@@ -20,6 +24,8 @@ using namespace oda;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kItems = 3;        // heads of a lane in flight
+constexpr int kMaxTok = 8;       // tokens of a block
 
 struct RopeArgs {
   const void* q;
@@ -33,7 +39,7 @@ struct RopeArgs {
   long long q_stride, k_stride, q_out_stride, k_out_stride;   // elements between tokens
   long long n;
   float eps;
-  int pos_offset, rot, hq, hkv;
+  int pos_offset, rot, hq, hkv, tok;
 };
 
 template <typename T>
@@ -70,91 +76,138 @@ __device__ __forceinline__ uint4 narrow<float>(const float* x) {
                     __float_as_uint(x[3]));
 }
 
-template <typename T, int D, int TOK, bool NEIGHBOURS>
+template <typename T, int D, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
-  constexpr int EPL = 16 / (int)sizeof(T);          // elements per lane
-  constexpr int LPH = D / EPL;                      // lanes per head
-  constexpr int GROUPS = kThreads / LPH;
-  __shared__ float2 turn[TOK][D / 2];               // (cos, sin)
+  constexpr int EPL = 16 / (int)sizeof(T);          // elements of a chunk
+  constexpr int NL = D / EPL / 2;                   // lanes per head, two chunks each
+  constexpr int GROUPS = kThreads / NL;
+  // (cos, sin) of two pairs in 16 bytes; a lane reads M of them a chunk, stored
+  // M apart so that neighbouring lanes read neighbouring 16 bytes
+  constexpr int M = NEIGHBOURS ? EPL / 4 : EPL / 2;
+  constexpr int UNITS = D / 4;
+  __shared__ float4 turn[kMaxTok][UNITS];
+  const auto slot = [](int u) { return u % M * (UNITS / M) + u / M; };
   pdl_wait();
   pdl_launch_dependents();
   const int half = a.rot / 2;
-  const long long j0 = (long long)blockIdx.x * TOK;
-  const int ntok = (int)min((long long)TOK, a.n - j0);
-  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-    const int tk = i / half, f = i - tk * half;
-    const double pos = (double)((long long)a.positions[j0 + tk] + a.pos_offset);
-    const double turns = pos * ((double)a.inv_freq[f] * 0.15915494309189533577);
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    turn[tk][f] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int li = threadIdx.x % LPH, grp = threadIdx.x / LPH;
-  const int e0 = li * EPL;
+  const long long j0 = (long long)blockIdx.x * a.tok;
+  const int ntok = (int)min((long long)a.tok, a.n - j0);
   const int heads = a.hq + (a.k ? a.hkv : 0);
-  const int lane = threadIdx.x & 31;
-  const bool rotated = e0 < a.rot;
-  const bool first = e0 < half;
-  // the lane of the same head that holds the other half of this lane's pairs
-  const int other = rotated ? lane + (first ? half / EPL : -(half / EPL)) : lane;
-  for (int base = 0; base < ntok * heads; base += GROUPS) {     // uniform over the block
-    const int it = base + grp;
-    const bool in = it < ntok * heads;
-    const int tk = in ? it / heads : 0;
-    const int h = in ? it - tk * heads : 0;
-    const bool is_k = h >= a.hq;
-    const T* src = is_k ? static_cast<const T*>(a.k) + (j0 + tk) * a.k_stride + (h - a.hq) * D
-                        : static_cast<const T*>(a.q) + (j0 + tk) * a.q_stride + h * D;
-    const T* wsrc = static_cast<const T*>(is_k ? a.k_weight : a.q_weight);
-    float x[EPL];
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in) v = *reinterpret_cast<const uint4*>(src + e0);
-    widen<T>(v, x);
-    // (every lane reduces: a warp may hold a head with a weight and one without)
-    float ss = 0.f;
+  const int li = threadIdx.x % NL, grp = threadIdx.x / NL;
+  // this lane's chunks: a pair of halves of the rotated part, or two behind it
+  const int pairs = half / EPL;
+  const bool rotated = li < pairs;
+  const int c0 = rotated ? li * EPL : a.rot + (li - pairs) * 2 * EPL;
+  const int c1 = rotated ? c0 + half : c0 + EPL;
+  int tk = grp / heads, h = grp - tk * heads;       // the group's first (token, head)
+  const int step_tk = GROUPS / heads, step_h = GROUPS - step_tk * heads;
+  bool first = true;
+  do {
+    uint4 v[kItems][2];
+    int itk[kItems], ih[kItems];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPH);
-    if (wsrc) {
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      float w[EPL];
-      widen<T>(*reinterpret_cast<const uint4*>(wsrc + e0), w);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = x[i] * r * w[i];
-    }
-    float y[EPL];
-    if (NEIGHBOURS) {
-#pragma unroll
-      for (int i = 0; i < EPL; i += 2) {
-        const float2 cs = rotated ? turn[tk][(e0 + i) / 2] : make_float2(1.f, 0.f);
-        y[i] = x[i] * cs.x - x[i + 1] * cs.y;
-        y[i + 1] = x[i + 1] * cs.x + x[i] * cs.y;
+    for (int u = 0; u < kItems; ++u) {
+      itk[u] = tk;
+      ih[u] = h;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (tk < ntok) {
+        const T* src = h >= a.hq ? static_cast<const T*>(a.k) + (j0 + tk) * a.k_stride + (h - a.hq) * D
+                                 : static_cast<const T*>(a.q) + (j0 + tk) * a.q_stride + h * D;
+        v[u][0] = *reinterpret_cast<const uint4*>(src + c0);
+        v[u][1] = *reinterpret_cast<const uint4*>(src + c1);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const float p = __shfl_sync(0xffffffffu, x[i], other);
-        const float2 cs = rotated ? turn[tk][first ? e0 + i : e0 + i - half] : make_float2(1.f, 0.f);
-        y[i] = first ? x[i] * cs.x - p * cs.y : x[i] * cs.x + p * cs.y;
-        if (!rotated) y[i] = x[i];
+      tk += step_tk;
+      h += step_h;
+      if (h >= heads) {
+        h -= heads;
+        ++tk;
       }
     }
-    if (in) {
-      T* dst = is_k ? static_cast<T*>(a.k_out) + (j0 + tk) * a.k_out_stride + (h - a.hq) * D
-                    : static_cast<T*>(a.q_out) + (j0 + tk) * a.q_out_stride + h * D;
-      *reinterpret_cast<uint4*>(dst + e0) = narrow<T>(y);
+    if (first) {
+      first = false;
+      for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
+        const int t = i / half, f = i - t * half;
+        const double pos = (double)((long long)a.positions[j0 + t] + a.pos_offset);
+        const double turns = pos * ((double)a.inv_freq[f] * 0.15915494309189533577);
+        float s, c;
+        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+        reinterpret_cast<float2*>(&turn[t][slot(f / 2)])[f & 1] = make_float2(c, s);
+      }
+      __syncthreads();
     }
-  }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      float x[2][EPL];
+      widen<T>(v[u][0], x[0]);
+      widen<T>(v[u][1], x[1]);
+      const bool is_k = ih[u] >= a.hq;
+      const T* w = static_cast<const T*>(is_k ? a.k_weight : a.q_weight);
+      // (every lane reduces: a warp may hold heads with a weight and without, or none)
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) ss = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], ss));
+#pragma unroll
+      for (int o = 1; o < NL; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, NL);
+      if (itk[u] >= ntok) continue;
+      if (w) {
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float wf[EPL];
+          widen<T>(*reinterpret_cast<const uint4*>(w + (p ? c1 : c0)), wf);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) x[p][i] = x[p][i] * r * wf[i];
+        }
+      }
+      if (rotated) {
+        const float4* tt = turn[itk[u]];
+        if (NEIGHBOURS) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int u0 = (p ? c1 : c0) / 4;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+              const float4 cs = tt[slot(u0 + m)];
+              float* y = x[p] + 4 * m;
+              const float y0 = y[0], y1 = y[1], y2 = y[2], y3 = y[3];
+              y[0] = y0 * cs.x - y1 * cs.y;
+              y[1] = y1 * cs.x + y0 * cs.y;
+              y[2] = y2 * cs.z - y3 * cs.w;
+              y[3] = y3 * cs.z + y2 * cs.w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const float4 cs = tt[slot(li * M + m)];
+            const float a0 = x[0][2 * m], a1 = x[0][2 * m + 1], b0 = x[1][2 * m], b1 = x[1][2 * m + 1];
+            x[0][2 * m] = a0 * cs.x - b0 * cs.y;
+            x[1][2 * m] = b0 * cs.x + a0 * cs.y;
+            x[0][2 * m + 1] = a1 * cs.z - b1 * cs.w;
+            x[1][2 * m + 1] = b1 * cs.z + a1 * cs.w;
+          }
+        }
+      }
+      T* dst = is_k ? static_cast<T*>(a.k_out) + (j0 + itk[u]) * a.k_out_stride + (ih[u] - a.hq) * D
+                    : static_cast<T*>(a.q_out) + (j0 + itk[u]) * a.q_out_stride + ih[u] * D;
+      *reinterpret_cast<uint4*>(dst + c0) = narrow<T>(x[0]);
+      *reinterpret_cast<uint4*>(dst + c1) = narrow<T>(x[1]);
+    }
+  } while (__any_sync(0xffffffffu, tk < ntok));
 }
 
 template <typename T, int D>
-oda_status launch_td(const RopeArgs& a, bool neighbours, cudaStream_t st) {
-  constexpr int TOK = 1;
-  const long long grid = ceil_div64(a.n, TOK);
+oda_status launch_td(RopeArgs& a, bool neighbours, int sms, cudaStream_t st) {
+  constexpr int GROUPS = kThreads / (D * (int)sizeof(T) / 32);
+  const int heads = a.hq + (a.k ? a.hkv : 0);
+  // as many tokens a block as its lanes hold at once, while the blocks still
+  // fill the SMs four times
+  a.tok = kItems * GROUPS / heads;
+  a.tok = a.tok < 1 ? 1 : a.tok > kMaxTok ? kMaxTok : a.tok;
+  while (a.tok > 1 && ceil_div64(a.n, a.tok) < 4ll * sms) --a.tok;
+  const long long grid = ceil_div64(a.n, a.tok);
   if (grid >= (1ll << 31)) return ODA_ERR_SHAPE;
-  auto k = neighbours ? qk_norm_rope_kernel<T, D, TOK, true> : qk_norm_rope_kernel<T, D, TOK, false>;
+  auto k = neighbours ? qk_norm_rope_kernel<T, D, true> : qk_norm_rope_kernel<T, D, false>;
   return launch_pdl(k, dim3((unsigned)grid), dim3(kThreads), 0, st, a) == cudaSuccess ? ODA_OK
                                                                                       : ODA_ERR_CUDA;
 }
@@ -190,10 +243,10 @@ oda_status launch_qk_norm_rope(oda_ctx* ctx, const void* q, int64_t q_stride, co
   a.hq = c.hq;
   a.hkv = c.hkv;
   if (c.dtype == ODA_BF16)
-    return c.head_dim == 128 ? launch_td<__nv_bfloat16, 128>(a, neighbours, st)
-                             : launch_td<__nv_bfloat16, 64>(a, neighbours, st);
-  return c.head_dim == 128 ? launch_td<float, 128>(a, neighbours, st)
-                           : launch_td<float, 64>(a, neighbours, st);
+    return c.head_dim == 128 ? launch_td<__nv_bfloat16, 128>(a, neighbours, ctx->num_sms, st)
+                             : launch_td<__nv_bfloat16, 64>(a, neighbours, ctx->num_sms, st);
+  return c.head_dim == 128 ? launch_td<float, 128>(a, neighbours, ctx->num_sms, st)
+                           : launch_td<float, 64>(a, neighbours, ctx->num_sms, st);
 }
 
 }  // namespace oda_impl
