@@ -7,31 +7,38 @@
 // The scales stay outside the products: a block's 16 tokens share them, so
 // kscale multiplies 16 scores and vscale 16 weights, never a code.
 //
-// Arithmetic. The codes (int8 or e4m3) are exact in f16, so both contractions
-// run as mma.sync m16n8k16 with f16 inputs and float32 sums, one 16-token block
-// (tile) at a time and one warp per tile:
-//   * q is brought into f16 exactly: a power of two per head puts its largest
-//     element into [1, 2) (an element below 2^-17 of that may lose its last
-//     bits, 2^-25 of the largest). A float32 q is split into two f16 parts.
-//   * the softmax weight w_j = 2^(s_j + log2 vscale - M + 14) is split into an
-//     f16 part and the f16 rest, 22 bits in all: columns 0-3 of the second
-//     product take the first parts of the (up to four) heads, columns 4-7 the
-//     rests. M is the running maximum of s_j + log2 vscale (what the value
-//     accumulators are relative to), kept apart from the maximum m of s_j (what
-//     the sum l is relative to): a block with a tiny scale then cannot push
-//     another block's weights out of f16.
-// Fragments come straight from 16-byte loads, with no transposition:
-//   * K (second operand, 16 dims x 8 columns): lane (n = lane / 4, tg = lane % 4)
-//     takes 16-byte chunk lane % 8 of row lane / 8. With d = 128 the two
-//     columns 2r, 2r+1 are the two halves of row r; rows 0-7 of the query
-//     operand hold the heads' first 64 dims and rows 8-15 the last 64, and a
-//     score is the sum of two accumulators of one lane. With d = 64 a 128-byte
-//     line holds two tokens, one per column.
-//   * V (first operand, 16 dims x 16 tokens): lane (g, tg) takes dims 16 g .. of
-//     its four tokens; token and dim orders are free as long as the weights
-//     and the output use the same ones.
-//   * the score accumulators of a lane are the weights it needs in the second
-//     product: probabilities never leave their lane.
+// Arithmetic, one 16-token block (tile) at a time and one warp per tile, with
+// the tokens as the products' 16 rows (scores) or depth (values):
+//   * Scores, e4m3: the codes become f16, exactly, and mma.sync m16n8k16 sums in
+//     float32. A power of two per head puts the query's largest element into
+//     [1, 2); it is then one f16 number (bfloat16: exact down to 2^-17 of the
+//     largest, and within 2^-25 of it below), or two (float32: the second is 2^11
+//     times what is left), in columns of their own.
+//   * Scores, int8: the codes go into mma.sync m16n8k32 as they are, so the query
+//     is written in whole numbers: a power of two per head makes its largest
+//     element 2^29 .. 2^30, and four balanced digits to the base 256 are four
+//     columns. The sums are exact; 2^-30 of the largest element is lost.
+//     (e4m3 products of that instruction are converted to f16 by the compiler,
+//     query and all, for each: 20 cycles against 16 for the two f16 products.)
+//   * The softmax weight times the value's scale, w_j = 2^(s_j - m) R with R =
+//     vscale 2^(m - M + 11), is split into an f16 part and the f16 rest, 22 bits
+//     in all, in two columns; the codes of V become f16. M is a reference for
+//     s_j + log2 vscale (what the value accumulators are relative to), kept apart
+//     from the reference m of s_j (what the sum l is relative to): a block with
+//     a tiny scale then cannot push another block's weights out of f16. Both are
+//     maxima when they are set, and set anew once a weight exceeds 16 times its
+//     reference, so most tiles need neither a maximum over lanes nor a rescaling.
+//   * A lane (g = lane / 4, tg = lane % 4) holds scores of one head and of the
+//     two tokens in rows g and g + 8; its columns of the second product are that
+//     head's, so references, sums and accumulators never leave their lane. The
+//     weights reach the second product's layout by an 8 x 8 transposition.
+// Fragments come straight from 16-byte loads:
+//   * K (first operand): chunks tg and tg + 4 (d = 128) of the lane's two tokens.
+//   * V (first operand, 16 dims x 16 tokens): D / 8 dims of tokens 4 tg .. 4 tg + 3,
+//     the tokens in rows 2 tg, 2 tg + 1, 2 tg + 8, 2 tg + 9. The eight lanes that
+//     shared memory serves together read four tokens, four rows apart: each four
+//     rows of V are a copy of their own, 32 bytes further than they would be,
+//     so that the lanes meet in no bank.
 #include "kv8.cuh"
 #include "plan.cuh"
 #include "tiles.cuh"
@@ -40,7 +47,9 @@ using namespace oda;
 
 namespace {
 
-constexpr int W = 8;                     // warps per CTA
+constexpr int W = 6;                     // warps per CTA
+constexpr int kBatch = 4;                // pairs of tiles of a warp looked up together, eight lanes each
+constexpr float kNone = -1e38f;          // a reference before any token: below every score
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per barrier wait
 
 struct Attn8Args {
@@ -73,6 +82,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transposed 8 x 8 matrix of 16-bit elements, two of a row in each lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // 8 bytes from global to shared memory whose arrival counts on a barrier.
 __device__ __forceinline__ void cp_async8_arrive(uint32_t dst, const void* src, uint32_t bar) {
   asm volatile(
@@ -81,242 +105,365 @@ __device__ __forceinline__ void cp_async8_arrive(uint32_t dst, const void* src, 
       : "memory");
 }
 
+// The whole warp waits for a barrier's phase; false: it gave up.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_long(bar, parity);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-
-// A lane's share of one tile: NI chunks of K, and four tokens' V.
+// V of a lane's four tokens; p: its place in the stage.
 template <int D>
-struct Tile {
-  static constexpr int NI = D / 32;      // K loads (lines of 128 bytes: 16 or 8 a tile)
-  static constexpr int VW = D / 32;      // 32-bit words of V per token and lane
-  static constexpr int MT = D / 16;      // 16-dim slices of the output
-  uint32_t k[NI][4];
-  uint32_t v[4][VW];
-};
-
-// The token (slot of the tile) of a lane's j-th score.
-template <int D>
-__device__ __forceinline__ int token_of(int tg, int j) {
-  return D == 128 ? tg + 4 * j : 2 * tg + (j & 1) + 8 * (j >> 1);
-}
-
-template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& t, const uint8_t* tile, int lane) {
-#pragma unroll
-  for (int i = 0; i < Tile<D>::NI; ++i) {
-    const uint4 x = *reinterpret_cast<const uint4*>(tile + i * 512 + lane * 16);
-    t.k[i][0] = x.x; t.k[i][1] = x.y; t.k[i][2] = x.z; t.k[i][3] = x.w;
-  }
-  const uint8_t* v = tile + ODA_TILE * D + (lane >> 2) * (D / 8);
+__device__ __forceinline__ void load_v(uint32_t (&v)[4][D / 32], const unsigned char* p, uint32_t mask,
+                                       int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint8_t* p = v + token_of<D>(lane & 3, j) * D;
-    if (D == 128) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
-      t.v[j][0] = x.x; t.v[j][1] = x.y; t.v[j][2 % Tile<D>::VW] = x.z; t.v[j][3 % Tile<D>::VW] = x.w;
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + j * D);
+      v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
     } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
-      t.v[j][0] = x.x; t.v[j][1] = x.y;
+      const uint2 x = *reinterpret_cast<const uint2*>(p + j * D);
+      v[j][0] = x.x; v[j][1] = x.y;
     }
+  }
+  if (mask != 0xffffu) {
+    // a slot outside may hold anything: a weight of 0 must not meet a NaN
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (!((mask >> (4 * (lane & 3) + j)) & 1u)) {
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) v[j][x] = 0u;
+      }
   }
 }
 
-// A warp's running state for one segment (row, KV head). Lane (g, tg): head
-// g % 4 for the statistics; of the accumulators, D / 8 dims of columns 2 tg, 2 tg + 1.
+// 16 elements of a query head.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float* x);
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+    bf16x2_to_f32(v.x, x[8 * i], x[8 * i + 1]);
+    bf16x2_to_f32(v.y, x[8 * i + 2], x[8 * i + 3]);
+    bf16x2_to_f32(v.z, x[8 * i + 4], x[8 * i + 5]);
+    bf16x2_to_f32(v.w, x[8 * i + 6], x[8 * i + 7]);
+  }
+}
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(p)[i];
+    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+  }
+}
+
+template <int D>
+struct Tile {
+  static constexpr int KC = D / 64;      // chunks of K per lane and column
+  static constexpr int VW = D / 32;      // 32-bit words of V per token and lane
+  static constexpr int MT = D / 16;      // 16-dim slices of the output
+  static constexpr int VG = 4 * D + 32;  // V's pitch of four tokens in a stage
+  static constexpr int BYTES = 2 * ODA_TILE * D;               // in the cache
+  static constexpr int STAGE = ODA_TILE * D + 4 * VG;          // in shared memory
+};
+
+constexpr float kLift = 11.f;            // weights are at most 2^15 < 65504
+
+// The head of a lane's scores, of a segment's up to two or four.
+__device__ __forceinline__ int head_of(int tg, bool wide) { return (tg >> 1) + (wide ? 2 * (tg & 1) : 0); }
+
+// A warp's running state for one segment (row, KV head).
 template <typename T, int D, int FMT>
 struct State {
-  uint32_t qf[4][4];                     // query operand: 4 slices of 16 dims a chunk
-  float qs;                              // score scale of this lane's head
-  float m, M, l;
-  float acc[Tile<D>::MT][4];
+  static constexpr int KC = Tile<D>::KC;
+  // second operand of the scores: products (int8: of two words, a set for two
+  // heads; e4m3: of one word)
+  uint32_t qf[4 * KC][2];
+  float qs;                              // this lane's head: what its sums count for, times the scores' scale
+  float m, M, l, K;                      // K = 2^(m - M + kLift), infinite while M is kNone
+  float acc[Tile<D>::MT][4];             // [0] + [1]: one dim of this lane's head, [2] + [3]: the next
 
   __device__ __forceinline__ void reset() {
-    m = M = -INFINITY;
+    m = M = kNone;
     l = 0.f;
+    K = INFINITY;
 #pragma unroll
     for (int i = 0; i < Tile<D>::MT; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
   }
 
+  // A head's elements of this lane's chunks over a power of two, 2^e <= largest < 2^(e+1).
+  __device__ __forceinline__ float load_head(const T* q, bool there, int tg, float (&x)[KC][16]) {
+    uint32_t top = 0;                    // |x| as bits: a NaN counts as the largest
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      if (there) {
+        load16<T>(q + (tg + 4 * c) * 16, x[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[c][i]) & 0x7fffffffu);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // (a query below 2^-100 counts from there; what is not finite makes every score NaN)
+    const int e = min(max((int)(top >> 23) - 127, -100), 127);
+    const float down = e == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[c][i] *= down;
+    return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+
   // q: the G query heads of the segment, [G][D]
   __device__ __forceinline__ void load_q(const T* q, int G, float qscale, int lane) {
-    const int g = lane >> 2, tg = lane & 3, h = g & 3;
-    constexpr int HALVES = D / 64;
-    float x[HALVES][16];
-    float top = 0.f;
+    const int g = lane >> 2, tg = lane & 3;
+    const bool wide = G > 2;
+    float x[KC][16];
+    if constexpr (FMT == kInt8) {        // column g: digit g % 4 of head g / 4, and of head 2 + g / 4
 #pragma unroll
-    for (int p = 0; p < HALVES; ++p)
+      for (int p = 0; p < 4 * KC; ++p) qf[p][0] = qf[p][1] = 0u;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[p][e] = h < G ? to_f32<T>(q[h * D + p * 64 + tg * 16 + e]) : 0.f;
-        top = fmaxf(top, fabsf(x[p][e]));
+      for (int set = 0; set < 2; ++set) {
+        if (set == 1 && !wide) break;
+        const int h = 2 * set + (g >> 2);
+        const float up = load_head(q + h * D, h < G, tg, x);
+        // y = d0 + 256 d1 + 256^2 d2 + 256^3 d3, each within -128 .. 127
+        const int sh = 8 * (g & 3);
+        const int carry = (int)(0x00808080u & ((1u << sh) - 1u));
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t dig = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dig |= (uint32_t)(((__float2int_rn(x[c][4 * w + i] * 0x1p29f) + carry) >> sh) & 255) << (8 * i);
+            qf[2 * KC * set + 2 * c + w / 2][w & 1] = dig;
+          }
+        // scores of the set's head tg / 2 come from the columns of g = 4 (tg / 2) ..
+        const float mine = __shfl_sync(0xffffffffu, up, (tg >> 1) * 16);
+        if (set == 0 || (tg & 1)) qs = qscale * 0x1p-29f * mine;
       }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^e <= top < 2^(e+1); no power for zeros and for what is not finite
-    int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-    e = e == 128 ? 0 : max(e, -100);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    qs = qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+    } else {                             // columns 2 t, 2 t + 1: the head of lanes tg = t, and its rest
+      const int h = head_of(g >> 1, wide);
+      const float up = load_head(q + h * D, h < G, tg, x);
 #pragma unroll
-    for (int p = 0; p < HALVES; ++p)
+      for (int c = 0; c < KC; ++c)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float y = x[p][i] * down;
-        // rows 4-7 repeat the heads; for a float32 query they hold the rest
-        if (sizeof(T) == 4 && g >= 4) y -= __half2float(__float2half_rn(y));
-        x[p][i] = y;
-      }
+        for (int w = 0; w < 4; ++w)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      qf[s][0] = pack_f16(x[0][4 * s], x[0][4 * s + 1]);
-      qf[s][2] = pack_f16(x[0][4 * s + 2], x[0][4 * s + 3]);
-      qf[s][1] = HALVES == 2 ? pack_f16(x[HALVES - 1][4 * s], x[HALVES - 1][4 * s + 1]) : 0u;
-      qf[s][3] = HALVES == 2 ? pack_f16(x[HALVES - 1][4 * s + 2], x[HALVES - 1][4 * s + 3]) : 0u;
+          for (int i = 0; i < 2; ++i) {
+            float y0 = x[c][4 * w + 2 * i], y1 = x[c][4 * w + 2 * i + 1];
+            if (g & 1) {
+              y0 = (y0 - __half2float(__float2half_rn(y0))) * 0x1p11f;
+              y1 = (y1 - __half2float(__float2half_rn(y1))) * 0x1p11f;
+            }
+            qf[4 * c + w][i] = pack_f16(y0, y1);
+          }
+      qs = qscale * __shfl_sync(0xffffffffu, up, tg * 8);
     }
   }
 
-  // One tile; `mask`: which of its 16 tokens take part (at least one).
-  __device__ __forceinline__ void tile(Tile<D>& t, uint32_t mask, float kscale, float vscale,
-                                       int lane) {
-    const int g = lane >> 2, tg = lane & 3;
-    float s[4];
+  // The scores of this lane's head with the tokens in rows g and g + 8, before the block's scale.
+  // (p_k: this lane's place in the stage's K)
+  __device__ __forceinline__ void scores(float (&s)[2], const unsigned char* p_k, bool wide, int tg) const {
+    uint32_t k[2][KC][4];
 #pragma unroll
-    for (int i = 0; i < Tile<D>::NI; ++i) {
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p_k + 2 * i * D + 64 * c);
+        k[i][c][0] = x.x; k[i][c][1] = x.y; k[i][c][2] = x.z; k[i][c][3] = x.w;
+      }
+    if constexpr (FMT == kInt8) {
+      // |sum| <= 2^21: the accumulators start at the bits of 1.5 * 2^23, and are floats as they stand
+      const float f = tg & 1 ? 65536.f : 1.f;
+      float v[2][2];
+#pragma unroll
+      for (int set = 0; set < 2; ++set) {
+        if (set == 1 && !wide) break;
+        int c[4] = {0x4b400000, 0x4b400000, 0x4b400000, 0x4b400000};
+#pragma unroll
+        for (int p = 0; p < 2 * KC; ++p)
+          mma16832(c, k[0][p / 2][p % 2 * 2], k[1][p / 2][p % 2 * 2], k[0][p / 2][p % 2 * 2 + 1],
+                   k[1][p / 2][p % 2 * 2 + 1], qf[2 * KC * set + p][0], qf[2 * KC * set + p][1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[set][i] = f * fmaf(__int_as_float(c[2 * i + 1]) - 0x1.8p23f, 256.f,
+                               __int_as_float(c[2 * i]) - 0x1.8p23f);
+      }
+      // the other two digits are the neighbour's
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float keep = v[0][i], send = v[0][i];
+        if (wide) {
+          if (tg & 1) keep = v[1][i]; else send = v[1][i];
+        }
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+      }
+    } else {
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t b0, b1;
-        Fmt8<FMT>::to_f16(t.k[i][w], b0, b1);
-        mma16816(c, qf[w][0], qf[w][1], qf[w][2], qf[w][3], b0, b1);
+      for (int p = 0; p < 4 * KC; ++p) {
+        uint32_t a0, a1, a2, a3;
+        Fmt8<FMT>::to_f16(k[0][p / 4][p % 4], a0, a2);
+        Fmt8<FMT>::to_f16(k[1][p / 4][p % 4], a1, a3);
+        mma16816(c, a0, a1, a2, a3, qf[p][0], qf[p][1]);
       }
-      if (D == 128) {
-        s[i] = c[0] + c[3];
-      } else {
-        s[2 * (i & 1)] = c[0];
-        s[2 * (i & 1) + 1] = c[1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        s[i] = sizeof(T) == 4 ? fmaf(c[2 * i + 1], 0x1p-11f, c[2 * i]) : c[2 * i];
+    }
+  }
+
+  // Two tiles' weights, as the second operand of the values' product; mask: which
+  // of a tile's 16 tokens take part.
+  __device__ __forceinline__ void weights(const float (&raw)[2][2], const uint32_t (&mask)[2],
+                                          const float2 (&scale)[2], uint32_t (&b)[2][2], int g) {
+    float s[2][2], e[2][2], w[2][2], R[2];
+    const bool whole = (mask[0] & mask[1]) == 0xffffu;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float sc = qs * scale[t].x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[t][i] = raw[t][i] * sc;
+      R[t] = scale[t].y == 0.f ? 0.f : scale[t].y * K;
+    }
+    if (!whole) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t mine = mask[t] >> (4 * (g >> 1) + (g & 1));
+        if (!(mine & 1u)) s[t][0] = -INFINITY;
+        if (!(mine & 4u)) s[t][1] = -INFINITY;
       }
     }
-    if (sizeof(T) == 4) {                // the two parts of a float32 query
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], 16);
-    }
-    const float sc = qs * kscale;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] *= sc;
-    if (mask != 0xffffu) {
+      for (int i = 0; i < 2; ++i) {
+        e[t][i] = fast_exp2(s[t][i] - m);
+        w[t][i] = e[t][i] * R[t];
+      }
+    const bool anew = fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[1][0], e[1][1])) > 16.f ||
+                      fmaxf(fmaxf(w[0][0], w[0][1]), fmaxf(w[1][0], w[1][1])) > 32768.f ||
+                      fmaxf(R[0], R[1]) > 0x1p100f;
+    if (__any_sync(0xffffffffu, anew)) {
+      float lv[2], top[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!((mask >> token_of<D>(tg, j)) & 1u)) {
-          s[j] = -INFINITY;
-          // a slot outside may hold anything: a weight of 0 must not meet a NaN
+      for (int t = 0; t < 2; ++t) {
+        lv[t] = fast_log2(scale[t].y);
+        top[t] = fmaxf(s[t][0], s[t][1]);
+        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 4));
+        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 8));
+        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 16));
+      }
+      const float m_new = fmaxf(m, fmaxf(top[0], top[1]));
+      const float M_new = fmaxf(M, fmaxf(top[0] + lv[0], top[1] + lv[1]));
+      const float alpha = fast_exp2(M - M_new);
 #pragma unroll
-          for (int w = 0; w < Tile<D>::VW; ++w) t.v[j][w] = 0u;
+      for (int i = 0; i < Tile<D>::MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] *= alpha;
+      l *= fast_exp2(m - m_new);
+      m = m_new;
+      M = M_new;
+      K = M == kNone ? INFINITY : fast_exp2(fminf(fmaxf(m - M + kLift, -126.f), 126.f));
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e[t][i] = fast_exp2(s[t][i] - m);
+          w[t][i] = fast_exp2(s[t][i] + (lv[t] - M + kLift));      // R may be out of range
         }
     }
-    float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float lv = fast_log2(vscale);
-    const float m_new = fmaxf(m, top), M_new = fmaxf(M, top + lv);
-    const float ms = m_new == -INFINITY ? 0.f : m_new;
-    const float Ms = M_new == -INFINITY ? 0.f : M_new;
-    if (__any_sync(0xffffffffu, M_new > M)) {
-      const float alpha = fast_exp2(M - Ms);              // M = -inf: 0
-      const float a0 = __shfl_sync(0xffffffffu, alpha, ((2 * tg) & 3) * 4);
-      const float a1 = __shfl_sync(0xffffffffu, alpha, ((2 * tg + 1) & 3) * 4);
+    l += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
+    // row g: this lane's two columns are the weight's f16 part and its rest
 #pragma unroll
-      for (int i = 0; i < Tile<D>::MT; ++i) {
-        acc[i][0] *= a0; acc[i][1] *= a1;
-        acc[i][2] *= a0; acc[i][3] *= a1;
-      }
-    }
-    l *= fast_exp2(m - ms);
-    m = m_new;
-    M = M_new;
-    float w[4];
-    const float shift = lv - Ms + 14.f;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      l += fast_exp2(s[j] - ms);
-      w[j] = fast_exp2(s[j] + shift);
-    }
-    // columns 0-3: the weights' f16 parts; 4-7: the rests
-    uint32_t b0 = pack_f16(w[0], w[1]), b1 = pack_f16(w[2], w[3]);
-    if (g >= 4) {
-      const float2 h0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
-      const float2 h1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
-      b0 = pack_f16(w[0] - h0.x, w[1] - h0.y);
-      b1 = pack_f16(w[2] - h1.x, w[3] - h1.y);
-    }
+      for (int i = 0; i < 2; ++i)
+        b[t][i] = transpose8x8(pack_f16(w[t][i], w[t][i] - __half2float(__float2half_rn(w[t][i]))));
+  }
+
+  __device__ __forceinline__ void values(const uint32_t (&v)[4][Tile<D>::VW], const uint32_t (&b)[2]) {
 #pragma unroll
     for (int x = 0; x < Tile<D>::VW; ++x) {
       // bytes of tokens 0 and 1 (2 and 3) of this lane side by side, per dim
-      const uint32_t p = __byte_perm(t.v[0][x], t.v[1][x], 0x5140);
-      const uint32_t q2 = __byte_perm(t.v[0][x], t.v[1][x], 0x7362);
-      const uint32_t r = __byte_perm(t.v[2][x], t.v[3][x], 0x5140);
-      const uint32_t u = __byte_perm(t.v[2][x], t.v[3][x], 0x7362);
+      const uint32_t p = __byte_perm(v[0][x], v[1][x], 0x5140);
+      const uint32_t q2 = __byte_perm(v[0][x], v[1][x], 0x7362);
+      const uint32_t r = __byte_perm(v[2][x], v[3][x], 0x5140);
+      const uint32_t u = __byte_perm(v[2][x], v[3][x], 0x7362);
       uint32_t a0, a1, a2, a3;
       Fmt8<FMT>::to_f16(p, a0, a1);
       Fmt8<FMT>::to_f16(r, a2, a3);
-      mma16816(acc[2 * x], a0, a1, a2, a3, b0, b1);
+      mma16816(acc[2 * x], a0, a1, a2, a3, b[0], b[1]);
       Fmt8<FMT>::to_f16(q2, a0, a1);
       Fmt8<FMT>::to_f16(u, a2, a3);
-      mma16816(acc[2 * x + 1], a0, a1, a2, a3, b0, b1);
+      mma16816(acc[2 * x + 1], a0, a1, a2, a3, b[0], b[1]);
     }
   }
 
   // This warp's (acc, M, m, l) for every head: ws [G][D + 4].
   __device__ __forceinline__ void store(float* ws, int G, int lane) {
     const int g = lane >> 2, tg = lane & 3;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const bool wide = G > 2;
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    const int h = head_of(tg, wide);
+    if (h >= G || (!wide && (tg & 1))) return;
+    float* w = ws + h * (D + 4);
 #pragma unroll
-    for (int i = 0; i < Tile<D>::MT; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float x = acc[i][c] + __shfl_xor_sync(0xffffffffu, acc[i][c], 2);
-        const int h = 2 * tg + (c & 1);
-        if (tg < 2 && h < G) ws[h * (D + 4) + g * (D / 8) + 2 * i + (c >> 1)] = x;
-      }
-    if (tg == 0 && g < G) {
-      ws[g * (D + 4) + D] = M;
-      ws[g * (D + 4) + D + 1] = m;
-      ws[g * (D + 4) + D + 2] = l;
+    for (int i = 0; i < Tile<D>::MT; ++i) {
+      w[g * (D / 8) + 2 * i] = acc[i][0] + acc[i][1];
+      w[g * (D / 8) + 2 * i + 1] = acc[i][2] + acc[i][3];
+    }
+    if (g == 0) {
+      w[D] = M;
+      w[D + 1] = m;
+      w[D + 2] = l;
     }
   }
 };
 
 // Shared memory of a launch, in order.
 struct Smem {
-  size_t wstate, rows, bars, scale, tile, bad, total;
+  size_t wstate, full, meta, rows, total;
+  // ns: stages of a pair of tiles per warp
   __host__ __device__ Smem(int G, int d, int max_batch, int ns) {
     const size_t state = (size_t)W * G * (d + 4) * 4, merge = (size_t)W * 32 * 6 * 4;
-    size_t at = (size_t)W * ns * 2 * ODA_TILE * d;           // stages
+    size_t at = (size_t)W * ns * 2 * (d == 128 ? Tile<128>::STAGE : Tile<64>::STAGE);
     wstate = at;                                             // [W][G][d + 4], or the merge's
     at += state > merge ? state : merge;
-    bars = at;                                               // [W][ns]
+    meta = at;                                               // [W][ns][2] Meta
+    at += (size_t)W * ns * 2 * 16;
+    full = at;                                               // [W][ns] barriers: a pair has landed
     at += (size_t)W * ns * 8;
-    scale = at;                                              // [W][ns] float2
-    at += (size_t)W * ns * 8;
-    tile = at;                                               // [W][ns] tile of each stage
-    at += (size_t)W * ns * 4;
-    bad = at;                                                // [W][ns] its block is out of range
-    at += (size_t)W * ns * 4;
     rows = at;                                               // 5 arrays by row slot
     at += (size_t)(5 * max_batch + 2) * 4;
     total = (at + 15) & ~(size_t)15;
   }
+};
+
+// What comes with a tile: its scales and which of its 16 tokens take part (0: none;
+// its block is out of range, or the pair has one tile only).
+struct __align__(16) Meta {
+  float2 scale;
+  uint32_t mask, unused;
 };
 
 // The last CTA of a segment puts its parts together. A thread takes four
@@ -324,7 +471,7 @@ struct Smem {
 template <typename T, int D>
 __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b, int g, int pbase,
                                             int nparts) {
-  constexpr int U = 10;
+  constexpr int U = 13;
   const int tid = threadIdx.x, G = a.G;
   const int nch = G * D / 4;                                 // 16 .. 128 chunks
   const int split = W * 32 / nch;
@@ -333,7 +480,7 @@ __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b
   const float* pml = a.partials + (size_t)a.max_parts * G * D;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = part; j0 < nparts; j0 += U * split) {
+  for (int j0 = part; part < split && j0 < nparts; j0 += U * split) {
     float2 ml[U];
     float4 v[U];
 #pragma unroll
@@ -390,13 +537,84 @@ __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b
   }
 }
 
+// The rows of a launch, worked out by one warp: the partition's head, and this
+// CTA's share in sinfo: {rows, tiles, CTAs, aligned, lo, hi, pbase, nparts, part}.
+__device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* sinfo, int* rowb,
+                                          int* rowt, int* rowstart, int* rowcs, int* rowlo) {
+  PlanIn p = {};
+  p.B = a.B;
+  p.count = a.count;
+  p.idx = a.idx;
+  p.seq_lens = a.seq_lens;
+  p.hkv = a.hkv;
+  p.max_blocks = a.max_blocks;
+  p.min_tiles = W;
+  p.slack = 3 * W;
+  p.grid = (int)gridDim.x;
+  p.err = a.err;
+  p.report = report && blockIdx.x == 0;
+  p.range_lo = a.range_lo;
+  p.range_hi = a.range_hi;
+  const PlanHead h = plan_rows(p, rowb, rowt, rowstart, rowcs, rowlo);
+  if ((threadIdx.x & 31) == 0) {
+    int o[5];
+    plan_cta((int)blockIdx.x, h, rowstart, rowcs, a.hkv, o);
+    sinfo[0] = h.nr; sinfo[1] = h.tot; sinfo[2] = h.P; sinfo[3] = h.al;
+    for (int i = 0; i < 5; ++i) sinfo[4 + i] = o[i];
+  }
+  __syncwarp();
+}
+
+// A walk over a CTA's share [lo, hi): the segment at hand (row slot i, KV head g, its
+// tiles [s1 - nt, s1) and those of them in the share, [x0, x1)), taken in pairs of
+// tiles, the last of which may hold one; `before`: the pairs of earlier segments.
+struct Walk {
+  int i, g, nt, s1, x0, x1, before;
+  __device__ __forceinline__ void start(const int* rowstart, int nr, int hkv, int lo, int hi) {
+    Cursor c;
+    locate(rowstart, nr, hkv, lo, c);
+    i = c.i; g = c.g; nt = c.nt; s1 = c.s1;
+    x0 = lo;
+    x1 = min(s1, hi);
+    before = 0;
+  }
+  __device__ __forceinline__ int pairs() const { return (x1 - x0 + 1) >> 1; }
+  // on to the next segment (there is one: x1 < hi)
+  __device__ __forceinline__ void next(const int* rowstart, int hkv, int hi) {
+    before += pairs();
+    do {
+      if (++g == hkv) {
+        g = 0;
+        ++i;
+        nt = (rowstart[i + 1] - rowstart[i]) / hkv;
+      }
+    } while (nt == 0);
+    x0 = s1;
+    s1 += nt;
+    x1 = min(s1, hi);
+  }
+  // on to pair p, which is not before this segment; false: there is none
+  __device__ __forceinline__ bool seek(const int* rowstart, int hkv, int hi, int p) {
+    while (p - before >= pairs()) {
+      if (x1 >= hi) return false;
+      next(rowstart, hkv, hi);
+    }
+    return true;
+  }
+};
+
 // A persistent grid takes the tiles as plan.cuh divides them; a CTA's share
-// may lie in one segment (row, KV head) or span several. Each warp streams
-// its own tiles, every W-th of the share, through a.ns stages of shared memory
-// with bulk copies, and runs ahead of its arithmetic across segments.
+// may lie in one segment (row, KV head) or span several. Warp w takes the share's
+// pairs of tiles w, w + W, ... and streams them through a.ns stages of shared memory
+// with bulk copies, running ahead of its arithmetic across segments. Two tiles at
+// a time are two independent chains of arithmetic: one alone left a warp waiting
+// for its own results two cycles of three. What a copy needs is worked out for
+// kBatch pairs at once, eight lanes a pair, one for each of its copies; the block ids
+// are looked up a batch ahead. (Tile by tile this cost as many instructions as
+// the arithmetic.)
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) {
-  constexpr int TILE = 2 * ODA_TILE * D;
+  constexpr int TILE = Tile<D>::BYTES, STAGE = Tile<D>::STAGE;
   extern __shared__ __align__(128) unsigned char smem[];
   const int G = a.G, ns = a.ns;
   const Smem lay(G, D, a.max_batch, ns);
@@ -409,142 +627,139 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   __shared__ int sinfo[9];
   __shared__ int slast;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned char* stages = smem + (size_t)warp * ns * TILE;
-  const uint32_t bars = smem_addr(smem + lay.bars + (size_t)warp * ns * 8);
-  float2* sscale = reinterpret_cast<float2*>(smem + lay.scale) + warp * ns;
-  int* stile = reinterpret_cast<int*>(smem + lay.tile) + warp * ns;
-  int* sbad = reinterpret_cast<int*>(smem + lay.bad) + warp * ns;
-  if (lane < ns) mbar_init(bars + 8 * lane, 2);    // the codes' bytes, the scales
+  const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
+  if (lane < ns) mbar_init(full + 8 * lane, 4);              // the codes' bytes and the scales of two tiles
   fence_mbar_init();
   if (!a.early) {
     pdl_wait();
     pdl_launch_dependents();
   }
-  if (warp == 0) {
-    PlanIn p = {};
-    p.B = a.B;
-    p.count = a.count;
-    p.idx = a.idx;
-    p.seq_lens = a.seq_lens;
-    p.hkv = a.hkv;
-    p.max_blocks = a.max_blocks;
-    p.min_tiles = W;
-    p.grid = (int)gridDim.x;
-    p.err = a.err;
-    p.report = blockIdx.x == 0;
-    p.range_lo = a.range_lo;
-    p.range_hi = a.range_hi;
-    const PlanHead h = plan_rows(p, rowb, rowt, rowstart, rowcs, rowlo);
-    if (lane == 0) {
-      int o[5];
-      plan_cta((int)blockIdx.x, h, rowstart, rowcs, a.hkv, o);
-      sinfo[0] = h.nr; sinfo[1] = h.tot; sinfo[2] = h.P; sinfo[3] = h.al;
-      for (int i = 0; i < 5; ++i) sinfo[4 + i] = o[i];
-    }
-  }
+  if (warp == 0) partition(a, true, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
   __syncthreads();
   const int nr = sinfo[0], total = sinfo[1], P = sinfo[2], aligned = sinfo[3];
   const int lo = sinfo[4], hi = sinfo[5];
-  const bool work = nr > 0 && total > 0 && lo < hi;
-  if (!work) {
+  if (!(nr > 0 && total > 0 && lo < hi)) {
     if (a.early) {
       pdl_wait();
       pdl_launch_dependents();
     }
     return;
   }
-  const uint64_t policy = l2_policy_evict_first();           // K/V is read once a launch
 
-  // ---- producer: the tiles of this warp, in order
-  Cursor prod;
-  prod.k = lo;
-  locate(rowstart, nr, a.hkv, lo, prod);
-  prod.k = min(lo + warp, hi);
-  normalize(rowstart, a.hkv, hi, warp, prod);
-  int bc_row = -1, bc_base = 0, bc_val = -1;                 // blocks of its next 32 tiles, one a lane
-  int pstage = 0, cstage = 0, flying = 0;
-  uint32_t parity = 0;
-  auto issue = [&]() {                                       // the next tile into stage pstage
-    const int jt = prod.k - (rowstart[prod.i] + prod.g * prod.nt);
-    if (prod.i != bc_row || jt < bc_base || jt >= bc_base + 32 * W || (jt - bc_base) % W != 0) {
-      bc_row = prod.i;
-      bc_base = jt;
-      const int jl = jt + lane * W;
-      bc_val = jl < prod.nt ? a.block_table[(long long)rowb[prod.i] * a.max_blocks +
-                                            (rowlo[prod.i] - 1) / ODA_TILE + jl]
-                            : -1;
-    }
-    const int blk = __shfl_sync(0xffffffffu, bc_val, (jt - bc_base) / W);
-    if (lane == 0) {
-      const uint32_t bar = bars + 8 * pstage;
-      const bool bad = blk < 0 || (long long)blk >= a.num_blocks;
-      stile[pstage] = prod.k;
-      sbad[pstage] = bad;
-      if (bad) {
-        record_error(a.err, ODA_ERR_BOUNDS);
-        mbar_arrive(bar);
-        mbar_arrive(bar);
-      } else {
-        const long long th = (long long)blk * a.hkv + prod.g;
-        mbar_arrive_expect_tx(bar, TILE);
-        bulk_g2s(smem_addr(stages + (size_t)pstage * TILE), a.codes + th * TILE, TILE, bar, policy);
-        cp_async8_arrive(smem_addr(sscale + pstage), a.scales + th * 2, bar);
-      }
-    }
-    pstage = pstage + 1 == ns ? 0 : pstage + 1;
-    ++flying;
-    prod.k += W;
-    normalize(rowstart, a.hkv, hi, warp, prod);
+  // ---- copies
+  const int tile = (lane >> 2) & 1, piece = lane & 3;        // this lane's copy of its pair
+  const uint64_t policy = l2_policy_evict_first();           // K/V is read once a launch
+  const unsigned char* stages = smem + (uint32_t)(warp * ns * 2 * STAGE);
+  Meta* meta = reinterpret_cast<Meta*>(smem + lay.meta) + warp * ns * 2;
+  const uint32_t to = smem_addr(stages) + tile * STAGE + (piece ? ODA_TILE * D + piece * Tile<D>::VG : 0);
+  const uint32_t from = piece ? ODA_TILE * D + piece * 4 * D : 0;
+  const uint32_t bytes = piece ? 4 * D : (ODA_TILE + 4) * D; // K and V's first four tokens; four of V
+  Walk at;
+  int pair = warp + W * (lane >> 3), blk = -1, jt = 0;       // of the next batch
+  bool there;
+  auto lookup = [&]() {
+    there = at.seek(rowstart, a.hkv, hi, pair);
+    const int k = at.x0 + 2 * (pair - at.before) + tile;
+    there = there && k < at.x1;
+    jt = k - (at.s1 - at.nt);
+    if (there)
+      blk = a.block_table[(long long)rowb[at.i] * a.max_blocks + (rowlo[at.i] - 1) / ODA_TILE + jt];
   };
-  for (int s = 0; s < ns && prod.k < hi; ++s) issue();
+  at.start(rowstart, nr, a.hkv, lo, hi);
+  int count;                                                 // this warp's pairs
+  {
+    Walk all = at;
+    while (all.x1 < hi) all.next(rowstart, a.hkv, hi);
+    count = (all.before + all.pairs() - warp + W - 1) / W;
+  }
+  lookup();
+  const uint8_t* src = nullptr;                              // of this batch
+  const float* ssrc = nullptr;
+  uint32_t mask = 0;
+  int issued = 0, islot = 0;
+  auto issue = [&]() {
+    if (issued % kBatch == 0) {
+      mask = 0;
+      if (there) {
+        const int first = rowlo[at.i], last = rowt[at.i];
+        const int base = (first - 1) / ODA_TILE * ODA_TILE;
+        const bool bad = blk < 0 || (long long)blk >= a.num_blocks;
+        const long long th = (long long)blk * a.hkv + at.g;
+        src = a.codes + th * TILE + from;
+        ssrc = a.scales + th * 2;
+        mask = bad ? 0u : range_bits(first - 1 - base, last - base, jt * ODA_TILE);
+        if (bad) record_error(a.err, ODA_ERR_BOUNDS);
+      }
+      pair += W * kBatch;
+      lookup();
+    }
+    if ((lane >> 3) == issued % kBatch) {
+      const uint32_t bar = full + 8 * islot;
+      if (piece == 0) {
+        Meta& mt = meta[2 * islot + tile];
+        mt.mask = mask;
+        if (mask) {
+          mbar_arrive_expect_tx(bar, TILE);
+          cp_async8_arrive(smem_addr(&mt.scale), ssrc, bar);
+        } else {
+          mt.scale = make_float2(0.f, 0.f);
+          mbar_arrive(bar);
+          mbar_arrive(bar);
+        }
+      }
+      if (mask) bulk_g2s(to + islot * 2 * STAGE, src, bytes, bar, policy);
+    }
+    ++issued;
+    islot = islot + 1 == ns ? 0 : islot + 1;
+  };
+  while (issued < ns && issued < count) issue();
   if (a.early) {
     pdl_wait();
     pdl_launch_dependents();
   }
+
+  // ---- segments of this CTA's share
   float* pacc = a.partials;
   float* pml = a.partials + (size_t)a.max_parts * G * D;
   const int hq = a.hkv * G;
+  const int lg = lane >> 2, tg = lane & 3;
+  const uint32_t k_at = (4 * (lg >> 1) + (lg & 1)) * D + tg * 16;
+  const uint32_t v_at = ODA_TILE * D + tg * Tile<D>::VG + lg * (D / 8);
+  int slot = 0, used = 0;
+  uint32_t parity = 0;
   bool aborted = false;
-  __syncwarp();
-
-  // ---- segments of this CTA's share
-  Cursor seg;
-  seg.k = lo;
-  locate(rowstart, nr, a.hkv, lo, seg);
+  Walk seg;
+  seg.start(rowstart, nr, a.hkv, lo, hi);
   while (true) {
-    const int b = rowb[seg.i], g = seg.g;
-    const int s0 = seg.s1 - seg.nt, s1 = seg.s1;
-    const int first = rowlo[seg.i], last = rowt[seg.i];
-    const int base = (first - 1) / ODA_TILE * ODA_TILE;
-    const int plo = first - 1 - base, phi = last - base;
+    const int b = rowb[seg.i], g = seg.g, s0 = seg.s1 - seg.nt, s1 = seg.s1;
     State<T, D, FMT> st;
     st.reset();
     st.load_q(static_cast<const T*>(a.q) + ((long long)b * hq + g * G) * D, G, a.qscale, lane);
-    while (flying > 0) {
-      const int k = stile[cstage];
-      if (k >= s1) break;                                    // of a later segment
-      if (!aborted) {
-        const bool ok = __all_sync(0xffffffffu,
-                                   mbar_wait_bounded(bars + 8 * cstage, parity, kWaitLimitNs));
-        if (!ok) {
-          aborted = true;
-          if (lane == 0) record_error(a.err, ODA_ERR_TIMEOUT);
-        }
+    for (const int end = seg.before + seg.pairs(); used * W + warp < end; ++used) {
+      if (aborted || !wait_phase(full + 8 * slot, parity)) {
+        if (!aborted && lane == 0) record_error(a.err, ODA_ERR_TIMEOUT);
+        aborted = true;
+        break;
       }
-      if (aborted) break;
-      const float2 sc = sscale[cstage];
-      const uint32_t mask = sbad[cstage] ? 0u : range_bits(plo, phi, (k - s0) * ODA_TILE);
-      Tile<D> t;
-      load_tile<D>(t, stages + (size_t)cstage * TILE, lane);
+      const Meta ma = meta[2 * slot], mb = meta[2 * slot + 1];
+      const unsigned char* stage = stages + (uint32_t)(slot * 2 * STAGE);
+      const uint32_t masks[2] = {ma.mask, mb.mask};
+      const float2 scales[2] = {ma.scale, mb.scale};
+      float raw[2][2];
+      uint32_t w[2][2], v[2][4][Tile<D>::VW];
+      st.scores(raw[0], stage + k_at, G > 2, tg);
+      st.scores(raw[1], stage + STAGE + k_at, G > 2, tg);
+      load_v<D>(v[0], stage + v_at, masks[0], lane);
+      load_v<D>(v[1], stage + STAGE + v_at, masks[1], lane);
       __syncwarp();                                          // every lane has its share
-      if (++cstage == ns) {
-        cstage = 0;
+      if (++slot == ns) {
+        slot = 0;
         parity ^= 1u;
       }
-      --flying;
-      if (prod.k < hi) issue();
-      if (mask) st.tile(t, mask, sc.x, sc.y, lane);
-      __syncwarp();                                          // stile, sbad of the tile just issued
+      if (issued < count) issue();
+      st.weights(raw, masks, scales, w, lg);
+      st.values(v[0], w[0]);
+      st.values(v[1], w[1]);
     }
     st.store(wstate + warp * G * (D + 4), G, lane);
     __syncthreads();
@@ -572,7 +787,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         const float* ws = wstate + (w * G + h) * (D + 4);
         if (ws[D + 2] == 0.f) continue;                // no token (a NaN is not left out)
         lt += ws[D + 2] * fast_exp2(ws[D + 1] - mt);
-        at += ws[dd] * fast_exp2(ws[D] - 14.f - mt);   // M = -inf: 0, or the NaN of a NaN scale
+        at += ws[dd] * fast_exp2(ws[D] - kLift - mt);  // M = -inf: 0, or the NaN of a NaN scale
       }
       if (nparts == 1) {
         static_cast<T*>(a.out)[((long long)b * hq + g * G + h) * D + dd] =
@@ -595,35 +810,28 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         if (tid == 0) a.tickets[sigma] = 0;
       }
     }
-    __syncthreads();
     if (s1 >= hi) break;
-    // the next segment with tiles
-    do {
-      if (++seg.g == a.hkv) {
-        seg.g = 0;
-        ++seg.i;
-        seg.nt = (rowstart[seg.i + 1] - rowstart[seg.i]) / a.hkv;
-      }
-    } while (seg.nt == 0);
-    seg.s1 = s1 + seg.nt;
+    __syncthreads();
+    seg.next(rowstart, a.hkv, hi);
   }
-  // never leave a copy landing in shared memory after exit (after a timeout
-  // the copies still flying are waited for once more, within the limit)
-  while (flying > 0) {
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + 8 * cstage, parity, kWaitLimitNs))) break;
-    if (++cstage == ns) {
-      cstage = 0;
-      parity ^= 1u;
+  // never leave a copy landing in shared memory after exit: after a timeout
+  // those still flying are waited for once more, within the limit
+  if (aborted) {
+    for (; used < issued; ++used) {
+      if (!wait_phase(full + 8 * slot, parity)) break;
+      if (++slot == ns) {
+        slot = 0;
+        parity ^= 1u;
+      }
     }
-    --flying;
   }
 }
 
-// Stages per warp: three where two CTAs of them fit an SM beside the row
-// arrays of a large batch, else two.
+// Stages per warp: two where two CTAs of them fit an SM beside the row arrays
+// of a large batch, else one.
 int stages_for(const oda_config& c) {
   const int G = c.hq / c.hkv;
-  return Smem(G, c.head_dim, c.max_batch, 3).total <= 112 * 1024 ? 3 : 2;
+  return Smem(G, c.head_dim, c.max_batch, 2).total <= 113 * 1024 - 128 ? 2 : 1;
 }
 
 size_t smem_bytes(const oda_config& c) {

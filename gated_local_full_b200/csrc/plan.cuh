@@ -9,7 +9,9 @@
 //     tiles) and every CTA works inside one segment;
 //   * even otherwise: the tile space is split evenly and a CTA may span
 //     several segments.
-// Aligned is used only if no CTA would get more than 1.2x the even share.
+// Aligned is used only if no CTA would get more than 1.2x the even share (or,
+// where the caller says so, few tiles more than it: then starting another
+// segment costs more than they do).
 //
 // plan_rows runs on warp 0 of a block and leaves the per-row arrays in shared
 // memory; plan_cta turns them into one CTA's share. Its global loads bypass
@@ -30,6 +32,7 @@ struct PlanIn {
   const int32_t* seq_lens;     // [B] t
   int hkv, sink, window, max_blocks;
   int min_tiles;               // smallest share of tiles per CTA
+  int slack = 0;                 // aligned too if no CTA gets this many tiles more than the even share
   int grid;                    // CTAs of the attention launch
   int* err;
   bool report;                 // record errors (one block per launch does)
@@ -144,7 +147,7 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
   h.nr = nr;
   h.tot = tot;
   h.P = P;
-  h.al = (tot > 0 && carry2 <= p.grid && 5 * worst <= 6 * even) ? 1 : 0;
+  h.al = (tot > 0 && carry2 <= p.grid && (5 * worst <= 6 * even || worst - even <= p.slack)) ? 1 : 0;
   return h;
 }
 
