@@ -49,6 +49,7 @@ namespace {
 
 constexpr int W = 6;                     // warps per CTA
 constexpr int kBatch = 4;                // pairs of tiles of a warp looked up together, eight lanes each
+constexpr int kAhead = 16;               // tiles of a CTA put into L2 before the dependency wait
 constexpr float kNone = -1e38f;          // a reference before any token: below every score
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per barrier wait
 
@@ -565,6 +566,26 @@ __device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* 
   __syncwarp();
 }
 
+// One warp: whether the lists still are those the partition was worked out from, and
+// raise no error. One round trip, since it needs no value to ask for the next.
+__device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo, const int* rowb,
+                                           const int* rowt, const int* rowlo) {
+  const int nr = sinfo[0];
+  bool same = __ldcg(a.count) == nr;
+  for (int i = threadIdx.x & 31; i < nr; i += 32) {
+    const int b = rowb[i];
+    const int t = __ldcg(a.seq_lens + b);
+    int first = 1, last = t;
+    if (a.range_lo) {
+      first = __ldcg(a.range_lo + b);
+      last = __ldcg(a.range_hi + b) - 1;
+    }
+    same = same && __ldcg(a.idx + i) == b && t >= 1 && first == rowlo[i] && last == rowt[i] &&
+           first >= 1 && last >= first && last <= t && (last - 1) / ODA_TILE < a.max_blocks;
+  }
+  return __all_sync(0xffffffffu, same);
+}
+
 // A walk over a CTA's share [lo, hi): the segment at hand (row slot i, KV head g, its
 // tiles [s1 - nt, s1) and those of them in the share, [x0, x1)), taken in pairs of
 // tiles, the last of which may hold one; `before`: the pairs of earlier segments.
@@ -630,11 +651,34 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
   if (lane < ns) mbar_init(full + 8 * lane, 4);              // the codes' bytes and the scales of two tiles
   fence_mbar_init();
+  bool guessed = false;
   if (!a.early) {
+    // Before the dependency wait: the partition from lists that the launch before may
+    // still be writing (every value is checked before it is used as an index), and
+    // this CTA's first tiles into L2. A prefetch reads no value, and after the wait
+    // the lists are compared, so a stale guess costs only time.
+    if (warp == 0) {
+      partition(a, false, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
+      guessed = true;
+      const int k = sinfo[4] + lane;
+      if (sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
+        Cursor c;
+        locate(rowstart, sinfo[0], a.hkv, k, c);
+        const int col = (rowlo[c.i] - 1) / ODA_TILE + k - (c.s1 - c.nt);
+        const int blk = col < a.max_blocks ? __ldcg(a.block_table + (long long)rowb[c.i] * a.max_blocks + col) : -1;
+        if (blk >= 0 && (long long)blk < a.num_blocks) {
+          const long long th = (long long)blk * a.hkv + c.g;
+          bulk_prefetch_l2(a.codes + th * TILE, TILE);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.scales + th * 2));
+        }
+      }
+      __syncwarp();
+    }
     pdl_wait();
     pdl_launch_dependents();
   }
-  if (warp == 0) partition(a, true, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
+  if (warp == 0 && !(guessed && same_lists(a, sinfo, rowb, rowt, rowlo)))
+    partition(a, true, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
   __syncthreads();
   const int nr = sinfo[0], total = sinfo[1], P = sinfo[2], aligned = sinfo[3];
   const int lo = sinfo[4], hi = sinfo[5];

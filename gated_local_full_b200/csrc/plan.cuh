@@ -87,7 +87,7 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
           first = rl;
           last = rh - 1;
         }
-        const int tend = (last + ODA_TILE - 1) / ODA_TILE;   // tiles up to the last position
+        const int tend = (last - 1) / ODA_TILE + 1;   // tiles up to the last position (>= 1)
         if (!ok || tend > p.max_blocks) {
           if (p.report) record_error(p.err, ODA_ERR_BOUNDS);
         } else {
