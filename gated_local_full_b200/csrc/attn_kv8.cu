@@ -486,14 +486,14 @@ __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b
     float4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * split;
-      ml[u] = make_float2(-INFINITY, 0.f);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j < nparts) {
-        ml[u] = __ldcg(reinterpret_cast<const float2*>(pml) + (long long)(pbase + j) * G + h);
-        v[u] = __ldcg(reinterpret_cast<const float4*>(a.partials + (long long)(pbase + j) * G * D) + ch);
-      }
+      // (past the last part the last one again, left out below: no branch between the loads)
+      const int j = min(j0 + u * split, nparts - 1);
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(pml) + (long long)(pbase + j) * G + h);
+      v[u] = __ldcg(reinterpret_cast<const float4*>(a.partials + (long long)(pbase + j) * G * D) + ch);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j0 + u * split >= nparts) ml[u].y = 0.f;
     float mt = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) mt = fmaxf(mt, ml[u].x);
@@ -549,8 +549,8 @@ __device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* 
   p.seq_lens = a.seq_lens;
   p.hkv = a.hkv;
   p.max_blocks = a.max_blocks;
-  p.min_tiles = W;
-  p.slack = 3 * W;
+  p.min_tiles = 2 * W;                   // a pair for every warp
+  p.slack = 6 * W;
   p.grid = (int)gridDim.x;
   p.err = a.err;
   p.report = report && blockIdx.x == 0;
@@ -820,29 +820,37 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       nparts = c_last - c_first + 1;
       mypart = (int)blockIdx.x + sigma;
     }
-    for (int o = tid; o < G * D; o += W * 32) {
-      const int h = o / D, dd = o % D;
+    if (tid < G * D / 4) {
+      const int h = tid * 4 / D, dd = tid * 4 % D;
+      const float* ws = wstate + h * (D + 4);
+      float4 tail[W];                                        // M, m, l of a warp
       float mt = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < W; ++w) mt = fmaxf(mt, wstate[(w * G + h) * (D + 4) + D + 1]);
-      float lt = 0.f, at = 0.f;
+      for (int w = 0; w < W; ++w) {
+        tail[w] = *reinterpret_cast<const float4*>(ws + w * G * (D + 4) + D);
+        mt = fmaxf(mt, tail[w].y);
+      }
+      float lt = 0.f;
+      float4 at4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float* ws = wstate + (w * G + h) * (D + 4);
-        if (ws[D + 2] == 0.f) continue;                // no token (a NaN is not left out)
-        lt += ws[D + 2] * fast_exp2(ws[D + 1] - mt);
-        at += ws[dd] * fast_exp2(ws[D] - kLift - mt);  // M = -inf: 0, or the NaN of a NaN scale
+        const float4 x = *reinterpret_cast<const float4*>(ws + w * G * (D + 4) + dd);
+        if (tail[w].z == 0.f) continue;                      // no token (a NaN is not left out)
+        lt += tail[w].z * fast_exp2(tail[w].y - mt);
+        const float f = fast_exp2(tail[w].x - kLift - mt);   // M = kNone: 0, or the NaN of a NaN scale
+        at4.x += x.x * f; at4.y += x.y * f; at4.z += x.z * f; at4.w += x.w * f;
       }
       if (nparts == 1) {
-        static_cast<T*>(a.out)[((long long)b * hq + g * G + h) * D + dd] =
-            (T)(lt != 0.f ? at / lt : 0.f);
+        const float inv = lt != 0.f ? 1.f / lt : 0.f;
+        const long long head = (long long)b * hq + g * G + h;
+        T* o = static_cast<T*>(a.out) + head * D + dd;
+        o[0] = (T)(at4.x * inv); o[1] = (T)(at4.y * inv); o[2] = (T)(at4.z * inv); o[3] = (T)(at4.w * inv);
         if (dd == 0 && a.lse)
-          a.lse[(long long)b * hq + g * G + h] =
-              lt != 0.f ? (mt + fast_log2(lt)) * 0.69314718055994531f : -INFINITY;
+          a.lse[head] = lt != 0.f ? (mt + fast_log2(lt)) * 0.69314718055994531f : -INFINITY;
       } else {
         const long long px = (long long)mypart * G + h;
-        pacc[px * D + dd] = at;
-        if (dd == 0) { pml[px * 2] = mt; pml[px * 2 + 1] = lt; }
+        *reinterpret_cast<float4*>(pacc + px * D + dd) = at4;
+        if (dd == 0) *reinterpret_cast<float2*>(pml + px * 2) = make_float2(mt, lt);
       }
     }
     if (nparts > 1) {
