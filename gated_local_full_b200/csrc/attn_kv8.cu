@@ -144,26 +144,23 @@ __device__ __forceinline__ void load_v(uint32_t (&v)[4][D / 32], const unsigned 
   }
 }
 
-// 16 elements of a query head.
+// 16 elements of a query head, as they lie in memory, in float32.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+__device__ __forceinline__ void widen16(const uint4* r, float* x) {
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-    bf16x2_to_f32(v.x, x[8 * i], x[8 * i + 1]);
-    bf16x2_to_f32(v.y, x[8 * i + 2], x[8 * i + 3]);
-    bf16x2_to_f32(v.z, x[8 * i + 4], x[8 * i + 5]);
-    bf16x2_to_f32(v.w, x[8 * i + 6], x[8 * i + 7]);
-  }
-}
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float* x) {
+    for (int i = 0; i < 2; ++i) {
+      bf16x2_to_f32(r[i].x, x[8 * i], x[8 * i + 1]);
+      bf16x2_to_f32(r[i].y, x[8 * i + 2], x[8 * i + 3]);
+      bf16x2_to_f32(r[i].z, x[8 * i + 4], x[8 * i + 5]);
+      bf16x2_to_f32(r[i].w, x[8 * i + 6], x[8 * i + 7]);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(p)[i];
-    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = __uint_as_float(r[i].x); x[4 * i + 1] = __uint_as_float(r[i].y);
+      x[4 * i + 2] = __uint_as_float(r[i].z); x[4 * i + 3] = __uint_as_float(r[i].w);
+    }
   }
 }
 
@@ -203,17 +200,34 @@ struct State {
       for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
   }
 
+  // The elements that this lane's columns need, asked for before they are wanted.
+  struct Query {
+    static constexpr int SETS = FMT == kInt8 ? 2 : 1;
+    uint4 r[SETS][KC][sizeof(T)];
+    // q: the G query heads of the segment, [G][D]
+    __device__ __forceinline__ void fetch(const T* q, int G, int lane) {
+      const int g = lane >> 2, tg = lane & 3;
+      const bool wide = G > 2;
+#pragma unroll
+      for (int set = 0; set < SETS; ++set) {
+        const int h = FMT == kInt8 ? 2 * set + (g >> 2) : head_of(g >> 1, wide);
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(T); ++i) {
+            r[set][c][i] = make_uint4(0, 0, 0, 0);
+            if (h < G) r[set][c][i] = reinterpret_cast<const uint4*>(q + h * D + (tg + 4 * c) * 16)[i];
+          }
+      }
+    }
+  };
+
   // A head's elements of this lane's chunks over a power of two, 2^e <= largest < 2^(e+1).
-  __device__ __forceinline__ float load_head(const T* q, bool there, int tg, float (&x)[KC][16]) {
+  __device__ __forceinline__ float scale_head(const uint4 (&r)[KC][sizeof(T)], float (&x)[KC][16]) {
     uint32_t top = 0;                    // |x| as bits: a NaN counts as the largest
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
-      if (there) {
-        load16<T>(q + (tg + 4 * c) * 16, x[c]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
-      }
+      widen16<T>(r[c], x[c]);
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[c][i]) & 0x7fffffffu);
     }
@@ -229,8 +243,7 @@ struct State {
     return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23);
   }
 
-  // q: the G query heads of the segment, [G][D]
-  __device__ __forceinline__ void load_q(const T* q, int G, float qscale, int lane) {
+  __device__ __forceinline__ void set_q(const Query& q, int G, float qscale, int lane) {
     const int g = lane >> 2, tg = lane & 3;
     const bool wide = G > 2;
     float x[KC][16];
@@ -240,8 +253,7 @@ struct State {
 #pragma unroll
       for (int set = 0; set < 2; ++set) {
         if (set == 1 && !wide) break;
-        const int h = 2 * set + (g >> 2);
-        const float up = load_head(q + h * D, h < G, tg, x);
+        const float up = scale_head(q.r[set % Query::SETS], x);
         // y = d0 + 256 d1 + 256^2 d2 + 256^3 d3, each within -128 .. 127
         const int sh = 8 * (g & 3);
         const int carry = (int)(0x00808080u & ((1u << sh) - 1u));
@@ -260,8 +272,7 @@ struct State {
         if (set == 0 || (tg & 1)) qs = qscale * 0x1p-29f * mine;
       }
     } else {                             // columns 2 t, 2 t + 1: the head of lanes tg = t, and its rest
-      const int h = head_of(g >> 1, wide);
-      const float up = load_head(q + h * D, h < G, tg, x);
+      const float up = scale_head(q.r[0], x);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -538,54 +549,6 @@ __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b
   }
 }
 
-// The rows of a launch, worked out by one warp: the partition's head, and this
-// CTA's share in sinfo: {rows, tiles, CTAs, aligned, lo, hi, pbase, nparts, part}.
-__device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* sinfo, int* rowb,
-                                          int* rowt, int* rowstart, int* rowcs, int* rowlo) {
-  PlanIn p = {};
-  p.B = a.B;
-  p.count = a.count;
-  p.idx = a.idx;
-  p.seq_lens = a.seq_lens;
-  p.hkv = a.hkv;
-  p.max_blocks = a.max_blocks;
-  p.min_tiles = 2 * W;                   // a pair for every warp
-  p.slack = 6 * W;
-  p.grid = (int)gridDim.x;
-  p.err = a.err;
-  p.report = report && blockIdx.x == 0;
-  p.range_lo = a.range_lo;
-  p.range_hi = a.range_hi;
-  const PlanHead h = plan_rows(p, rowb, rowt, rowstart, rowcs, rowlo);
-  if ((threadIdx.x & 31) == 0) {
-    int o[5];
-    plan_cta((int)blockIdx.x, h, rowstart, rowcs, a.hkv, o);
-    sinfo[0] = h.nr; sinfo[1] = h.tot; sinfo[2] = h.P; sinfo[3] = h.al;
-    for (int i = 0; i < 5; ++i) sinfo[4 + i] = o[i];
-  }
-  __syncwarp();
-}
-
-// One warp: whether the lists still are those the partition was worked out from, and
-// raise no error. One round trip, since it needs no value to ask for the next.
-__device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo, const int* rowb,
-                                           const int* rowt, const int* rowlo) {
-  const int nr = sinfo[0];
-  bool same = __ldcg(a.count) == nr;
-  for (int i = threadIdx.x & 31; i < nr; i += 32) {
-    const int b = rowb[i];
-    const int t = __ldcg(a.seq_lens + b);
-    int first = 1, last = t;
-    if (a.range_lo) {
-      first = __ldcg(a.range_lo + b);
-      last = __ldcg(a.range_hi + b) - 1;
-    }
-    same = same && __ldcg(a.idx + i) == b && t >= 1 && first == rowlo[i] && last == rowt[i] &&
-           first >= 1 && last >= first && last <= t && (last - 1) / ODA_TILE < a.max_blocks;
-  }
-  return __all_sync(0xffffffffu, same);
-}
-
 // A walk over a CTA's share [lo, hi): the segment at hand (row slot i, KV head g, its
 // tiles [s1 - nt, s1) and those of them in the share, [x0, x1)), taken in pairs of
 // tiles, the last of which may hold one; `before`: the pairs of earlier segments.
@@ -624,6 +587,62 @@ struct Walk {
   }
 };
 
+// The rows of a launch, worked out by one warp: the partition's head, and this
+// CTA's share in sinfo: {rows, tiles, CTAs, aligned, lo, hi, pbase, nparts, part,
+// pairs}, and the walk at its start.
+__device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* sinfo, Walk* walk, int* rowb,
+                                          int* rowt, int* rowstart, int* rowcs, int* rowlo) {
+  PlanIn p = {};
+  p.B = a.B;
+  p.count = a.count;
+  p.idx = a.idx;
+  p.seq_lens = a.seq_lens;
+  p.hkv = a.hkv;
+  p.max_blocks = a.max_blocks;
+  p.min_tiles = 2 * W;                   // a pair for every warp
+  p.slack = 6 * W;
+  p.grid = (int)gridDim.x;
+  p.err = a.err;
+  p.report = report && blockIdx.x == 0;
+  p.range_lo = a.range_lo;
+  p.range_hi = a.range_hi;
+  const PlanHead h = plan_rows(p, rowb, rowt, rowstart, rowcs, rowlo);
+  if ((threadIdx.x & 31) == 0) {
+    int o[5];
+    plan_cta((int)blockIdx.x, h, rowstart, rowcs, a.hkv, o);
+    sinfo[0] = h.nr; sinfo[1] = h.tot; sinfo[2] = h.P; sinfo[3] = h.al;
+    for (int i = 0; i < 5; ++i) sinfo[4 + i] = o[i];
+    if (h.nr > 0 && h.nr <= a.B && o[0] >= 0 && o[0] < o[1] && o[1] <= h.tot) {
+      Walk w;
+      w.start(rowstart, h.nr, a.hkv, o[0], o[1]);
+      *walk = w;
+      while (w.x1 < o[1]) w.next(rowstart, a.hkv, o[1]);
+      sinfo[9] = w.before + w.pairs();
+    }
+  }
+  __syncwarp();
+}
+
+// One warp: whether the lists still are those the partition was worked out from, and
+// raise no error. One round trip, since it needs no value to ask for the next.
+__device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo, const int* rowb,
+                                           const int* rowt, const int* rowlo) {
+  const int nr = sinfo[0];
+  bool same = __ldcg(a.count) == nr;
+  for (int i = threadIdx.x & 31; i < nr; i += 32) {
+    const int b = rowb[i];
+    const int t = __ldcg(a.seq_lens + b);
+    int first = 1, last = t;
+    if (a.range_lo) {
+      first = __ldcg(a.range_lo + b);
+      last = __ldcg(a.range_hi + b) - 1;
+    }
+    same = same && __ldcg(a.idx + i) == b && t >= 1 && first == rowlo[i] && last == rowt[i] &&
+           first >= 1 && last >= first && last <= t && (last - 1) / ODA_TILE < a.max_blocks;
+  }
+  return __all_sync(0xffffffffu, same);
+}
+
 // A persistent grid takes the tiles as plan.cuh divides them; a CTA's share
 // may lie in one segment (row, KV head) or span several. Warp w takes the share's
 // pairs of tiles w, w + W, ... and streams them through a.ns stages of shared memory
@@ -645,7 +664,8 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   int* rowb = rowcs + a.max_batch + 1;                                 // [max_batch] each
   int* rowt = rowb + a.max_batch;
   int* rowlo = rowt + a.max_batch;
-  __shared__ int sinfo[9];
+  __shared__ int sinfo[10];
+  __shared__ Walk swalk;
   __shared__ int slast;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
@@ -658,7 +678,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
     // this CTA's first tiles into L2. A prefetch reads no value, and after the wait
     // the lists are compared, so a stale guess costs only time.
     if (warp == 0) {
-      partition(a, false, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
+      partition(a, false, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
       guessed = true;
       const int k = sinfo[4] + lane;
       if (sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
@@ -678,7 +698,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
     pdl_launch_dependents();
   }
   if (warp == 0 && !(guessed && same_lists(a, sinfo, rowb, rowt, rowlo)))
-    partition(a, true, sinfo, rowb, rowt, rowstart, rowcs, rowlo);
+    partition(a, true, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
   __syncthreads();
   const int nr = sinfo[0], total = sinfo[1], P = sinfo[2], aligned = sinfo[3];
   const int lo = sinfo[4], hi = sinfo[5];
@@ -709,13 +729,15 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
     if (there)
       blk = a.block_table[(long long)rowb[at.i] * a.max_blocks + (rowlo[at.i] - 1) / ODA_TILE + jt];
   };
-  at.start(rowstart, nr, a.hkv, lo, hi);
-  int count;                                                 // this warp's pairs
-  {
-    Walk all = at;
-    while (all.x1 < hi) all.next(rowstart, a.hkv, hi);
-    count = (all.before + all.pairs() - warp + W - 1) / W;
-  }
+  at = swalk;
+  const int count = (sinfo[9] - warp + W - 1) / W;           // this warp's pairs
+  Walk seg = swalk;
+  const int hq = a.hkv * G;
+  typename State<T, D, FMT>::Query query;
+  auto fetch = [&]() {
+    query.fetch(static_cast<const T*>(a.q) + ((long long)rowb[seg.i] * hq + seg.g * G) * D, G, lane);
+  };
+  if (!a.early) fetch();                                     // before the lookup: it is wanted no later
   lookup();
   const uint8_t* src = nullptr;                              // of this batch
   const float* ssrc = nullptr;
@@ -760,25 +782,23 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   if (a.early) {
     pdl_wait();
     pdl_launch_dependents();
+    fetch();
   }
 
   // ---- segments of this CTA's share
   float* pacc = a.partials;
   float* pml = a.partials + (size_t)a.max_parts * G * D;
-  const int hq = a.hkv * G;
   const int lg = lane >> 2, tg = lane & 3;
   const uint32_t k_at = (4 * (lg >> 1) + (lg & 1)) * D + tg * 16;
   const uint32_t v_at = ODA_TILE * D + tg * Tile<D>::VG + lg * (D / 8);
   int slot = 0, used = 0;
   uint32_t parity = 0;
   bool aborted = false;
-  Walk seg;
-  seg.start(rowstart, nr, a.hkv, lo, hi);
   while (true) {
     const int b = rowb[seg.i], g = seg.g, s0 = seg.s1 - seg.nt, s1 = seg.s1;
     State<T, D, FMT> st;
     st.reset();
-    st.load_q(static_cast<const T*>(a.q) + ((long long)b * hq + g * G) * D, G, a.qscale, lane);
+    st.set_q(query, G, a.qscale, lane);
     for (const int end = seg.before + seg.pairs(); used * W + warp < end; ++used) {
       if (aborted || !wait_phase(full + 8 * slot, parity)) {
         if (!aborted && lane == 0) record_error(a.err, ODA_ERR_TIMEOUT);
@@ -865,6 +885,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
     if (s1 >= hi) break;
     __syncthreads();
     seg.next(rowstart, a.hkv, hi);
+    fetch();
   }
   // never leave a copy landing in shared memory after exit: after a timeout
   // those still flying are waited for once more, within the limit
