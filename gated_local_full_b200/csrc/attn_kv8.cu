@@ -667,6 +667,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   __shared__ int sinfo[10];
   __shared__ Walk swalk;
   __shared__ int slast;
+  __shared__ int waited;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
   if (lane < ns) mbar_init(full + 8 * lane, 4);              // the codes' bytes and the scales of two tiles
@@ -677,11 +678,17 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
     // still be writing (every value is checked before it is used as an index), and
     // this CTA's first tiles into L2. A prefetch reads no value, and after the wait
     // the lists are compared, so a stale guess costs only time.
+    // (A CTA that started late, the wait already over, leaves the prefetch out.)
+    if (warp == 1) {
+      if (lane == 0) *const_cast<volatile int*>(&waited) = 0;
+      pdl_wait();
+      if (lane == 0) *const_cast<volatile int*>(&waited) = 1;
+    }
     if (warp == 0) {
       partition(a, false, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
       guessed = true;
       const int k = sinfo[4] + lane;
-      if (sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
+      if (!*const_cast<volatile int*>(&waited) && sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
         Cursor c;
         locate(rowstart, sinfo[0], a.hkv, k, c);
         const int col = (rowlo[c.i] - 1) / ODA_TILE + k - (c.s1 - c.nt);
