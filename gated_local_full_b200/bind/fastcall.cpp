@@ -1,0 +1,293 @@
+// The binding's calls that a decode loop makes once or more a layer, in C++.
+//
+// A launch takes the host 2.6 us; the same call through ctypes, with its checks
+// in Python, 8 to 12: a tensor's attribute costs 0.05 to 0.15 us from Python, a
+// converted argument 0.1, and a call has 10 to 20 of them. Here a tensor is read
+// directly, and the C entry point is called through its address, which the
+// binding takes from the library that it loaded.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/oda.h"
+
+namespace {
+
+enum Fn { kAppend, kRead, kFull, kRange, kRope, kFns };
+void* g_fn[kFns];
+PyObject* g_error = nullptr;             // OdaError(status, where)
+
+struct Refused {};                       // a Python error is set
+
+[[noreturn]] void refuse(const char* what) {
+  PyErr_SetString(PyExc_ValueError, what);
+  throw Refused();
+}
+
+long long number(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Refused();
+  return v;
+}
+
+// A tensor, or null for None.
+const at::Tensor* tensor(PyObject* o, const char* what) {
+  if (o == Py_None) return nullptr;
+  if (!THPVariable_Check(o)) refuse(what);
+  return &THPVariable_Unpack(o);
+}
+
+void* data(const at::Tensor& x) {
+  if (!x.is_cuda()) refuse("tensor must live on the GPU");
+  return x.data_ptr();
+}
+
+// Device pointer of a tensor (CUDA and contiguous), an int, or None.
+void* ptr(PyObject* o) {
+  if (o == Py_None) return nullptr;
+  if (PyLong_Check(o)) {
+    void* p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Refused();
+    return p;
+  }
+  const at::Tensor* x = tensor(o, "a tensor, an address or None is wanted");
+  if (!x->is_cuda()) refuse("tensor must live on the GPU");
+  if (!x->is_contiguous()) refuse("tensor must be contiguous");
+  return x->data_ptr();
+}
+
+// Several of them, in order (before the stream is asked for: it needs a GPU, and a
+// tensor that is not on one is the better thing to report).
+template <int N>
+struct Ptrs {
+  void* p[N];
+  Ptrs(PyObject* const* a) {
+    for (int i = 0; i < N; ++i) p[i] = ptr(a[i]);
+  }
+  const int32_t* ints(int i) const { return static_cast<const int32_t*>(p[i]); }
+  float* floats(int i) const { return static_cast<float*>(p[i]); }
+};
+
+void* stream(PyObject* o) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
+  if (PyLong_Check(o)) return ptr(o);
+  PyObject* s = PyObject_GetAttrString(o, "cuda_stream");
+  if (!s) throw Refused();
+  void* p = PyLong_AsVoidPtr(s);
+  Py_DECREF(s);
+  if (!p && PyErr_Occurred()) throw Refused();
+  return p;
+}
+
+int format(PyObject* o) {
+  if (PyUnicode_Check(o)) {
+    if (PyUnicode_CompareWithASCIIString(o, "int8") == 0) return ODA_KV8_INT8;
+    if (PyUnicode_CompareWithASCIIString(o, "e4m3") == 0) return ODA_KV8_E4M3;
+    return 0;                            // refused by the library, as any other number
+  }
+  return (int)number(o);
+}
+
+// The context: (handle, hq, hkv, head_dim, dtype).
+struct Ctx {
+  oda_ctx* h;
+  long long hq, hkv, d;
+  at::ScalarType type;
+};
+Ctx context(PyObject* o) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) refuse("not a context");
+  Ctx c;
+  c.h = static_cast<oda_ctx*>(ptr(PyTuple_GET_ITEM(o, 0)));
+  c.hq = number(PyTuple_GET_ITEM(o, 1));
+  c.hkv = number(PyTuple_GET_ITEM(o, 2));
+  c.d = number(PyTuple_GET_ITEM(o, 3));
+  c.type = number(PyTuple_GET_ITEM(o, 4)) == ODA_BF16 ? at::kBFloat16 : at::kFloat;
+  return c;
+}
+
+PyObject* done(int status, const char* where) {
+  if (status == ODA_OK) Py_RETURN_NONE;
+  PyObject* e = PyObject_CallFunction(g_error, "is", status, where);
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  return nullptr;
+}
+
+template <typename F>
+PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
+  if (n != want) {
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return nullptr;
+  }
+  try {
+    return f();
+  } catch (const Refused&) {
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// n_tokens of a [layers][n_tokens][hkv][d] tensor of the context's dtype.
+long long tokens(const Ctx& c, const at::Tensor& x, long long layers, const char* dtype, const char* shape) {
+  if (x.scalar_type() != c.type) refuse(dtype);
+  if (x.dim() != 4 || x.size(0) != layers || x.size(2) != c.hkv || x.size(3) != c.d) refuse(shape);
+  return x.size(1);
+}
+
+// ctx, format, layer_begin, layer_end, k_new, v_new, tok_start, seq_lens, block_table, codes, scales,
+// ring, B, stream
+PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const Ctx c = context(a[0]);
+    const long long lb = number(a[2]), le = number(a[3]);
+    const at::Tensor* k = tensor(a[4], "k_new must be a tensor");
+    const at::Tensor* v = tensor(a[5], "v_new must be a tensor");
+    if (!k || !v) refuse("k_new and v_new must be tensors");
+    const long long nt = tokens(c, *k, le - lb, "k_new must have the context's dtype",
+                                "k_new must be [layers][n_tokens][hkv][d]");
+    if (v->sizes() != k->sizes() || v->scalar_type() != k->scalar_type())
+      refuse("k_new and v_new differ in shape or type");
+    const Ptrs<8> p(a + 4);
+    void* st = stream(a[13]);
+    auto f = reinterpret_cast<decltype(&oda_append_kv8)>(g_fn[kAppend]);
+    return done(f(c.h, format(a[1]), (int)lb, (int)le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4),
+                  p.p[5], p.floats(6), p.p[7], (int)number(a[12]), st),
+                "oda_append_kv8");
+  });
+}
+
+// ctx, format, layer_begin, layer_end, tok_start, seq_lens, block_table, codes, scales, k_out, v_out,
+// B, stream
+PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const Ctx c = context(a[0]);
+    const long long lb = number(a[2]), le = number(a[3]);
+    const at::Tensor* k = tensor(a[9], "k_out must be a tensor or None");
+    const at::Tensor* v = tensor(a[10], "v_out must be a tensor or None");
+    if (!k && !v) refuse("read_kv8 needs k_out or v_out");
+    long long nt = 0;
+    if (k)
+      nt = tokens(c, *k, le - lb, "k_out must have the context's dtype",
+                  "k_out must be [layers][n_tokens][hkv][d]");
+    if (v) {
+      const long long m = tokens(c, *v, le - lb, "v_out must have the context's dtype",
+                                 "v_out must be [layers][n_tokens][hkv][d]");
+      if (k && m != nt) refuse("k_out and v_out differ in length");
+      nt = m;
+    }
+    const Ptrs<7> p(a + 4);
+    void* st = stream(a[12]);
+    auto f = reinterpret_cast<decltype(&oda_read_kv8)>(g_fn[kRead]);
+    return done(f(c.h, format(a[1]), (int)lb, (int)le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3],
+                  p.floats(4), p.p[5], p.p[6], (int)number(a[11]), st),
+                "oda_read_kv8");
+  });
+}
+
+// ctx, format, layer, q, seq_lens, block_table, codes, scales, idx, count, out, lse, B, flags, stream
+PyObject* full_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const Ctx c = context(a[0]);
+    const Ptrs<9> p(a + 3);
+    void* st = stream(a[14]);
+    auto f = reinterpret_cast<decltype(&oda_full_attn_kv8)>(g_fn[kFull]);
+    return done(f(c.h, format(a[1]), (int)number(a[2]), p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4),
+                  p.ints(5), p.ints(6), p.p[7], p.floats(8), (int)number(a[12]), (unsigned)number(a[13]), st),
+                "oda_full_attn_kv8");
+  });
+}
+
+// ctx, format, layer, q, seq_lens, range_lo, range_hi, block_table, codes, scales, idx, count, out,
+// lse, B, flags, stream
+PyObject* range_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const Ctx c = context(a[0]);
+    const Ptrs<11> p(a + 3);
+    void* st = stream(a[16]);
+    auto f = reinterpret_cast<decltype(&oda_range_attn_kv8)>(g_fn[kRange]);
+    return done(f(c.h, format(a[1]), (int)number(a[2]), p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4),
+                  p.p[5], p.floats(6), p.ints(7), p.ints(8), p.p[9], p.floats(10), (int)number(a[14]),
+                  (unsigned)number(a[15]), st),
+                "oda_range_attn_kv8");
+  });
+}
+
+// An [n][heads][d] tensor of the context's dtype with a token's heads contiguous.
+void check_heads(const Ctx& c, const at::Tensor& x, long long n, long long heads) {
+  if (x.scalar_type() != c.type || x.dim() != 3 || x.size(0) != n || x.size(1) != heads ||
+      x.size(2) != c.d)
+    refuse("q and k must be [n][hq][d] and [n][hkv][d] of the context's dtype");
+}
+void* heads(const Ctx& c, const at::Tensor& x, long long& token_stride) {
+  void* p = data(x);
+  if (x.stride(2) != 1 || (x.stride(1) != c.d && x.size(1) > 1))
+    refuse("the heads of a token must be contiguous");
+  // one token's stride says nothing (and may be anything): its heads' extent does
+  token_stride = x.size(0) > 1 ? x.stride(0) : x.size(1) * c.d;
+  return p;
+}
+
+// ctx, q, k, q_weight, k_weight, eps, inv_freq, positions, q_out, k_out, pos_offset, flags, stream
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 13, [&]() -> PyObject* {
+    const Ctx c = context(a[0]);
+    const at::Tensor* q = tensor(a[1], "q must be a tensor");
+    const at::Tensor* qo = tensor(a[8], "q_out must be a tensor");
+    if (!q || !qo) refuse("q and q_out must be tensors");
+    const at::Tensor* k = tensor(a[2], "k must be a tensor or None");
+    const at::Tensor* ko = tensor(a[9], "k_out must be a tensor or None");
+    const long long n = q->dim() > 0 ? q->size(0) : -1;
+    for (int i = 3; i < 5; ++i) {
+      const at::Tensor* w = tensor(a[i], "a norm weight must be a tensor or None");
+      if (w && (w->scalar_type() != c.type || w->numel() != c.d))
+        refuse("a norm weight must be [d] of the context's dtype");
+    }
+    const at::Tensor* fr = tensor(a[6], "inv_freq must be a tensor or None");
+    const at::Tensor* pos = tensor(a[7], "positions must be a tensor or None");
+    if (fr && (fr->scalar_type() != at::kFloat || !pos || pos->scalar_type() != at::kInt || pos->numel() != n))
+      refuse("inv_freq must be float32, positions int32 [n]");
+    check_heads(c, *q, n, c.hq);
+    check_heads(c, *qo, n, c.hq);
+    if (k) check_heads(c, *k, n, c.hkv);
+    if (ko) check_heads(c, *ko, n, c.hkv);
+    long long qs, qos, ks = 0, kos = 0;
+    void* qp = heads(c, *q, qs);
+    void* qop = heads(c, *qo, qos);
+    void* kp = k ? heads(c, *k, ks) : nullptr;
+    void* kop = ko ? heads(c, *ko, kos) : nullptr;
+    const Ptrs<2> w(a + 3), fp(a + 6);
+    const double eps = PyFloat_AsDouble(a[5]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Refused();
+    void* st = stream(a[12]);
+    auto f = reinterpret_cast<decltype(&oda_qk_norm_rope)>(g_fn[kRope]);
+    return done(f(c.h, qp, qs, kp, ks, w.p[0], w.p[1], (float)eps, fp.floats(0),
+                  fr ? (int)(2 * fr->numel()) : 0, fp.ints(1), (int)number(a[10]), n, qop, qos, kop, kos,
+                  (unsigned)number(a[11]), st),
+                "oda_qk_norm_rope");
+  });
+}
+
+// bind(error class, addresses in the order of Fn)
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 1 + kFns, [&]() -> PyObject* {
+    Py_INCREF(a[0]);
+    Py_XSETREF(g_error, a[0]);
+    for (int i = 0; i < kFns; ++i) g_fn[i] = ptr(a[1 + i]);
+    Py_RETURN_NONE;
+  });
+}
+
+#define ODA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {ODA_METHOD(append_kv8),    ODA_METHOD(read_kv8),     ODA_METHOD(full_attn_kv8),
+                         ODA_METHOD(range_attn_kv8), ODA_METHOD(qk_norm_rope), ODA_METHOD(bind),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&module); }

@@ -1,4 +1,5 @@
-"""Build liboda.so (and the synthetic-input fill library) in-tree for sm_100a.
+"""Build liboda.so (and the synthetic-input fill library) in-tree for sm_100a, and
+the binding's compiled calls.
 
     python -m gated_local_full_b200.build [--verbose]
 
@@ -60,13 +61,38 @@ def _build_lib(name: str, src_dir: str, out_dir: str, verbose: bool, extra=()) -
     return lib
 
 
+def _build_fastcall() -> str:
+    """The CPython module of the binding's compiled calls, against this interpreter's torch."""
+    import sysconfig
+    import torch
+    t = os.path.dirname(torch.__file__)
+    lib = os.path.join(PKG, "_fastcall.so")
+    tmp = lib + ".tmp"
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"),
+           os.path.join(PKG, "bind", "fastcall.cpp"), "-o", tmp, "-L", os.path.join(t, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for the compiled calls:\n{r.stderr}")
+    os.replace(tmp, lib)
+    return lib
+
+
 def build(verbose: bool = False) -> list:
-    """Compile liboda.so and libsynth.so; returns their paths."""
+    """Compile liboda.so, libsynth.so and the binding's calls; returns their paths."""
     inc = ["-I", os.path.join(ROOT, "include")]
-    oda = _build_lib("liboda.so", os.path.join(PKG, "csrc"), PKG, verbose, inc)
-    syn_dir = os.path.join(ROOT, "synth")
-    syn = _build_lib("libsynth.so", os.path.join(syn_dir, "csrc"), syn_dir, verbose)
-    return [oda, syn]
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        bind = ex.submit(_build_fastcall)
+        oda = _build_lib("liboda.so", os.path.join(PKG, "csrc"), PKG, verbose, inc)
+        syn_dir = os.path.join(ROOT, "synth")
+        syn = _build_lib("libsynth.so", os.path.join(syn_dir, "csrc"), syn_dir, verbose)
+        return [oda, syn, bind.result()]
 
 
 if __name__ == "__main__":

@@ -23,7 +23,6 @@ OK, ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS, ERR_STATE 
 BF16, F32 = 0, 1
 MAX_BATCH = 1024
 KV8_INT8, KV8_E4M3 = 1, 2  # formats of the 8-bit paged cache
-KV8_FORMATS = {"int8": KV8_INT8, "e4m3": KV8_E4M3}
 ROPE_NEIGHBOURS = 1       # oda_qk_norm_rope flag
 ATTN_INPUTS_READY = 1     # oda_local_attn / oda_full_attn_gated flag (see oda.h)
 # A step with at least this many layers runs the recall head's first layer over
@@ -209,29 +208,26 @@ def kv8_layout(cfg: OdaConfig) -> dict:
     return {k: int(getattr(info, k)) for k, _ in OdaKv8LayoutInfo._fields_}
 
 
-def _format(f) -> int:
-    return KV8_FORMATS.get(f, f)
+_fast = None
+_FAST_CALLS = ("oda_append_kv8", "oda_read_kv8", "oda_full_attn_kv8", "oda_range_attn_kv8",
+               "oda_qk_norm_rope")
 
 
-def _dtype(cfg):
-    import torch
-    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
-
-
-def _check_heads(x, shape, dtype):
-    if x.dtype is not dtype or x.shape != shape:
-        raise ValueError("q and k must be [n][hq][d] and [n][hkv][d] of the context's dtype")
-
-
-def _heads(x, n, heads, d):
-    """(pointer, token stride) of an [n][heads][d] tensor whose heads are contiguous."""
-    if not x.is_cuda:
-        raise ValueError("tensor must live on the GPU")
-    tokens, head, one = x.stride()
-    if one != 1 or (head != d and heads > 1):
-        raise ValueError("the heads of a token must be contiguous")
-    # one token's stride says nothing (and may be anything): its heads' extent does
-    return x.data_ptr(), tokens if n > 1 else heads * d
+def _fastcall():
+    """The calls of a decode loop's 8-bit cache, compiled (bind/fastcall.cpp): 4 to 5 us
+    a call against 8 to 12 through ctypes with the checks in Python."""
+    global _fast
+    if _fast is None:
+        import torch  # noqa: F401  (its libraries, which the module needs)
+        try:
+            from . import _fastcall as f
+        except ImportError as e:
+            raise RuntimeError("_fastcall.so is missing or does not load: build it with "
+                               "`python -m gated_local_full_b200.build` (no fallback exists)") from e
+        L = lib()
+        f.bind(OdaError, *[ctypes.cast(getattr(L, n), c_void_p).value for n in _FAST_CALLS])
+        _fast = f
+    return _fast
 
 
 class OdaGraph:
@@ -278,6 +274,7 @@ class OdaContext:
         self.handle = h
 
     def close(self) -> None:
+        self._key = None
         if self.handle:
             lib().oda_destroy(self.handle)
             self.handle = None
@@ -287,6 +284,15 @@ class OdaContext:
             self.close()
         except Exception:
             pass
+
+    _key = None
+
+    def _context(self):
+        """(handle, hq, hkv, head_dim, dtype) for the compiled calls."""
+        if self._key is None:
+            c = self.cfg
+            self._key = (self.handle.value if self.handle else None, c.hq, c.hkv, c.head_dim, c.dtype)
+        return self._key
 
     # ------------------------------------------------------------- the path
     def append_kv(self, layer_begin, layer_end, k_new, v_new, seq_lens, block_table, kv_cache,
@@ -362,66 +368,37 @@ class OdaContext:
 
     # ------------------------------------------------------ the 8-bit cache
     # format: "int8" or "e4m3" (or KV8_INT8, KV8_E4M3)
-    def _tokens(self, x, layer_begin, layer_end, what):
-        """The shape of an [layers][n_tokens][hkv][d] tensor of the context's dtype."""
-        c = self.cfg
-        if x.dtype is not _dtype(c):
-            raise ValueError(f"{what} must have the context's dtype")
-        shape = x.shape
-        if len(shape) != 4 or shape[0] != layer_end - layer_begin or shape[2] != c.hkv or \
-                shape[3] != c.head_dim:
-            raise ValueError(f"{what} must be [layers][n_tokens][hkv][d]")
-        return shape
-
     def append_kv8(self, format, layer_begin, layer_end, k_new, v_new, seq_lens, block_table,
                    codes, scales, ring, B, tok_start=None, stream=None):
         """Quantise the rows' new tokens into the 8-bit cache, and into the ring as
-        they are (oda_append_kv8). tok_start: None for one token a row."""
-        shape = self._tokens(k_new, layer_begin, layer_end, "k_new")
-        if v_new.shape != shape or v_new.dtype is not k_new.dtype:
-            raise ValueError("k_new and v_new differ in shape or type")
-        _check(lib().oda_append_kv8(self.handle, _format(format), layer_begin, layer_end,
-                                    ptr(k_new), ptr(v_new), ptr(tok_start), shape[1], ptr(seq_lens),
-                                    ptr(block_table), ptr(codes), ptr(scales), ptr(ring), B,
-                                    _stream(stream)), "oda_append_kv8")
+        they are (oda_append_kv8). k_new, v_new [layers][n_tokens][hkv][d];
+        tok_start: None for one token a row."""
+        (_fast or _fastcall()).append_kv8(
+            self._key or self._context(), format, layer_begin, layer_end, k_new, v_new, tok_start,
+            seq_lens, block_table, codes, scales, ring, B, stream)
 
     def read_kv8(self, format, layer_begin, layer_end, seq_lens, block_table, codes, scales,
                  k_out, v_out, B, tok_start=None, stream=None):
         """The rows' positions up to seq_lens out of the 8-bit cache (oda_read_kv8);
         k_out or v_out may be None."""
-        shape = None
-        if k_out is not None:
-            shape = self._tokens(k_out, layer_begin, layer_end, "k_out")
-        if v_out is not None:
-            other = self._tokens(v_out, layer_begin, layer_end, "v_out")
-            if shape is not None and other != shape:
-                raise ValueError("k_out and v_out differ in length")
-            shape = other
-        if shape is None:
-            raise ValueError("read_kv8 needs k_out or v_out")
-        _check(lib().oda_read_kv8(self.handle, _format(format), layer_begin, layer_end,
-                                  ptr(tok_start), shape[1], ptr(seq_lens), ptr(block_table),
-                                  ptr(codes), ptr(scales), ptr(k_out), ptr(v_out), B,
-                                  _stream(stream)), "oda_read_kv8")
+        (_fast or _fastcall()).read_kv8(
+            self._key or self._context(), format, layer_begin, layer_end, tok_start, seq_lens,
+            block_table, codes, scales, k_out, v_out, B, stream)
 
     def full_attn_kv8(self, format, layer, q, seq_lens, block_table, codes, scales, idx, count,
                       out, lse, B, stream=None, inputs_ready=False):
         """full_attn_gated over the 8-bit cache (oda_full_attn_kv8)."""
-        _check(lib().oda_full_attn_kv8(self.handle, _format(format), layer, ptr(q), ptr(seq_lens),
-                                       ptr(block_table), ptr(codes), ptr(scales), ptr(idx),
-                                       ptr(count), ptr(out), ptr(lse), B,
-                                       ATTN_INPUTS_READY if inputs_ready else 0,
-                                       _stream(stream)), "oda_full_attn_kv8")
+        (_fast or _fastcall()).full_attn_kv8(
+            self._key or self._context(), format, layer, q, seq_lens, block_table, codes, scales,
+            idx, count, out, lse, B, ATTN_INPUTS_READY if inputs_ready else 0, stream)
 
     def range_attn_kv8(self, format, layer, q, seq_lens, range_lo, range_hi, block_table, codes,
                        scales, idx, count, out, lse, B, stream=None, inputs_ready=False):
         """range_attn over the 8-bit cache (oda_range_attn_kv8)."""
-        _check(lib().oda_range_attn_kv8(self.handle, _format(format), layer, ptr(q),
-                                        ptr(seq_lens), ptr(range_lo), ptr(range_hi),
-                                        ptr(block_table), ptr(codes), ptr(scales), ptr(idx),
-                                        ptr(count), ptr(out), ptr(lse), B,
-                                        ATTN_INPUTS_READY if inputs_ready else 0,
-                                        _stream(stream)), "oda_range_attn_kv8")
+        (_fast or _fastcall()).range_attn_kv8(
+            self._key or self._context(), format, layer, q, seq_lens, range_lo, range_hi,
+            block_table, codes, scales, idx, count, out, lse, B,
+            ATTN_INPUTS_READY if inputs_ready else 0, stream)
 
     def qk_norm_rope(self, q, k, q_weight, k_weight, eps, inv_freq, positions, q_out, k_out,
                      pos_offset=0, interleaved=False, stream=None):
@@ -429,35 +406,9 @@ class OdaContext:
         (oda_qk_norm_rope). q [n][hq][d], k [n][hkv][d] or None, with any token
         stride; inv_freq float32 [rot_dim / 2] or None for the norm alone;
         interleaved: pairs are neighbours instead of halves apart."""
-        c = self.cfg
-        d, dtype = c.head_dim, _dtype(c)
-        n = q.shape[0]
-        for w in (q_weight, k_weight):
-            if w is not None and (w.dtype is not dtype or w.numel() != d):
-                raise ValueError("a norm weight must be [d] of the context's dtype")
-        rot = 0
-        if inv_freq is not None:
-            import torch
-            rot = 2 * inv_freq.numel()
-            if inv_freq.dtype is not torch.float32 or positions is None or \
-                    positions.dtype is not torch.int32 or positions.numel() != n:
-                raise ValueError("inv_freq must be float32, positions int32 [n]")
-        hq, hkv = c.hq, c.hkv
-        _check_heads(q, (n, hq, d), dtype)
-        _check_heads(q_out, (n, hq, d), dtype)
-        if k is not None:
-            _check_heads(k, (n, hkv, d), dtype)
-        if k_out is not None:
-            _check_heads(k_out, (n, hkv, d), dtype)
-        qp, qs = _heads(q, n, hq, d)
-        qo, qos = _heads(q_out, n, hq, d)
-        kp, ks = (None, 0) if k is None else _heads(k, n, hkv, d)
-        ko, kos = (None, 0) if k_out is None else _heads(k_out, n, hkv, d)
-        _check(lib().oda_qk_norm_rope(self.handle, qp, qs, kp, ks, ptr(q_weight), ptr(k_weight),
-                                      float(eps), ptr(inv_freq), rot, ptr(positions),
-                                      int(pos_offset), n, qo, qos, ko, kos,
-                                      ROPE_NEIGHBOURS if interleaved else 0, _stream(stream)),
-               "oda_qk_norm_rope")
+        (_fast or _fastcall()).qk_norm_rope(
+            self._key or self._context(), q, k, q_weight, k_weight, eps, inv_freq, positions,
+            q_out, k_out, pos_offset, ROPE_NEIGHBOURS if interleaved else 0, stream)
 
     def get_device_error(self, stream=None) -> int:
         e = c_int(0)
