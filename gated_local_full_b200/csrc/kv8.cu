@@ -42,9 +42,11 @@ struct Kv8Args {
   int* err;
 };
 
-constexpr int kThreads = 256;
-// One, two and four units: 28 layers x 32 rows of one token written and read back
-// 17.2, 14.7 and 15.6 us, 8 x 16K tokens read 124.6, 126.2 and 126.1 us.
+// Blocks of 64, 128 and 256 threads: 28 layers x 32 rows written and read back 16.0, 14.0
+// and 14.8 us, a 16K prefill 32.4, 32.4 and 33.8, ragged float32 chunks 5.2, 5.7 and 6.8.
+constexpr int kThreads = 128;
+// One, two and four units (in blocks of 256 threads): 28 layers x 32 rows written and
+// read back 17.2, 14.7 and 15.6 us, 8 x 16K tokens read 124.6, 126.2 and 126.1 us.
 constexpr int kReadUnits = 2;
 
 struct Item {
@@ -62,26 +64,39 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
   long long ts = it, n = 1;
   m.b = (int)it;
   if (a.tok_start) {
-    int b = 0;
-    for (int base = 0; base < a.B; base += 32) {      // the last row that starts at or before it
+    // the last row that starts at or before it; all that is needed of a row is
+    // asked for at once
+    int b = 0, r_ts = 0, r_te = 0, r_t = 0;
+    for (int base = 0; base < a.B; base += 32) {
       const int r = base + lane;
-      const bool in = r < a.B && (long long)__ldg(a.tok_start + r) / ODA_TILE + 2ll * r <= (long long)it;
-      const unsigned who = __ballot_sync(0xffffffffu, in);
+      int v_ts = 0, v_te = 0, v_t = 0;
+      if (r < a.B) {
+        v_ts = __ldg(a.tok_start + r);
+        v_te = __ldg(a.tok_start + r + 1);
+        v_t = __ldg(a.seq_lens + r);
+      }
+      const unsigned who = __ballot_sync(
+          0xffffffffu, r < a.B && (long long)v_ts / ODA_TILE + 2ll * r <= (long long)it);
       if (!who) break;
-      b = base + 31 - __clz(who);
+      const int at = 31 - __clz(who);
+      b = base + at;
+      r_ts = __shfl_sync(0xffffffffu, v_ts, at);
+      r_te = __shfl_sync(0xffffffffu, v_te, at);
+      r_t = __shfl_sync(0xffffffffu, v_t, at);
     }
     m.b = b;
-    ts = __ldg(a.tok_start + b);
-    const long long te = __ldg(a.tok_start + b + 1);
-    n = te - ts;
-    if (ts < 0 || n < 0 || te > a.n_tokens) {
+    m.t = r_t;
+    ts = r_ts;
+    n = (long long)r_te - ts;
+    if (ts < 0 || n < 0 || r_te > a.n_tokens) {
       record_error(a.err, ODA_ERR_BOUNDS);
       return false;
     }
     if (n == 0) return false;
     j = (int)((long long)it - (ts / ODA_TILE + 2ll * b));
+  } else {
+    m.t = __ldg(a.seq_lens + m.b);
   }
-  m.t = __ldg(a.seq_lens + m.b);
   const long long past = m.t - n;               // positions before the call's
   if (m.t < 1 || past < 0) {
     record_error(a.err, ODA_ERR_BOUNDS);
@@ -234,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kv8_kernel(const Kv8Args 
 }
 
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_kv8_kernel(const Kv8Args a) {
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 1024 : 512) / kThreads) append_kv8_kernel(const Kv8Args a) {
   using R = Rows<T, D>;
   pdl_wait();
   pdl_launch_dependents();
@@ -288,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_kv8_k
 }
 
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads, D * sizeof(T) <= 256 ? 4 : 3) read_kv8_kernel(const Kv8Args a) {
+__global__ void __launch_bounds__(kThreads, (D * sizeof(T) <= 256 ? 1024 : 768) / kThreads) read_kv8_kernel(const Kv8Args a) {
   using R = Rows<T, D>;
   constexpr int U = kReadUnits, NW = R::EPL / 4;
   pdl_wait();
