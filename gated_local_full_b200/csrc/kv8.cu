@@ -193,14 +193,14 @@ __device__ __forceinline__ void rescale_codes(uint8_t* tile, int words, int lane
 // A token's chunk of one head into the ring: its slot of the window, and of the
 // sinks. pos is 0-indexed, t the row's last position, ring the head's chunk.
 template <typename T, int D>
-__device__ __forceinline__ void store_ring(const Kv8Args& a, T* ring, long long pos, int t, int kv,
+__device__ __forceinline__ void store_ring(const Kv8Args& a, T* ring, int pos, int t, int kv,
                                            const uint4 x) {
   if (pos >= (long long)t - a.window) {
-    const int w = a.sink + (int)(pos % a.window);
+    const int w = a.sink + pos % a.window;
     *reinterpret_cast<uint4*>(ring + ((long long)(w / ODA_TILE * 2 + kv) * ODA_TILE + w % ODA_TILE) * D) = x;
   }
   if (pos < a.sink)
-    *reinterpret_cast<uint4*>(ring + ((pos / ODA_TILE * 2 + kv) * ODA_TILE + pos % ODA_TILE) * D) = x;
+    *reinterpret_cast<uint4*>(ring + ((long long)(pos / ODA_TILE * 2 + kv) * ODA_TILE + pos % ODA_TILE) * D) = x;
 }
 
 template <typename T, int D>
@@ -291,13 +291,14 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 1024 : 512) / kThr
     const int s = p * R::RPP + rr;
     if (s >= m.s0 && s < m.s1) store_codes<T, FMT>(tile + s * D + li * R::EPL, x[p], inv);
   }
-  if (a.ring) {
+  // (most blocks of a long chunk lie before the window)
+  if (a.ring && (m.col * ODA_TILE < a.sink || (m.col + 1ll) * ODA_TILE > (long long)m.t - a.window)) {
     T* ring = ring_chunk<T, D>(a, l, m.b, g, li);
 #pragma unroll
     for (int p = 0; p < R::PASSES; ++p) {
       const int s = p * R::RPP + rr;
       if (s >= m.s0 && s < m.s1)
-        store_ring<T, D>(a, ring, (long long)m.col * ODA_TILE + s, m.t, kv, x[p]);
+        store_ring<T, D>(a, ring, m.col * ODA_TILE + s, m.t, kv, x[p]);
     }
   }
 }

@@ -37,10 +37,13 @@ struct Fmt8<kInt8> {
     lo = *reinterpret_cast<uint32_t*>(&x);
     hi = *reinterpret_cast<uint32_t*>(&y);
   }
-  // four float32 -> four codes
+  // four float32 within +-127 -> four codes: added to 1.5 * 2^23 they are rounded to
+  // whole numbers, ties to even, in the sum's low byte
   static __device__ __forceinline__ uint32_t pack(float x, float y, float z, float w) {
-    const uint32_t a = __byte_perm((uint32_t)__float2int_rn(x), (uint32_t)__float2int_rn(y), 0x0040);
-    const uint32_t b = __byte_perm((uint32_t)__float2int_rn(z), (uint32_t)__float2int_rn(w), 0x0040);
+    const uint32_t a = __byte_perm(__float_as_uint(__fadd_rn(x, 0x1.8p23f)),
+                                   __float_as_uint(__fadd_rn(y, 0x1.8p23f)), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(__fadd_rn(z, 0x1.8p23f)),
+                                   __float_as_uint(__fadd_rn(w, 0x1.8p23f)), 0x0040);
     return __byte_perm(a, b, 0x5410);
   }
 };
