@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -39,8 +40,11 @@ const at::Tensor* tensor(PyObject* o, const char* what) {
   return &THPVariable_Unpack(o);
 }
 
+// Device pointer of a tensor on the current device (the library refuses a context of
+// another one).
 void* data(const at::Tensor& x) {
   if (!x.is_cuda()) refuse("tensor must live on the GPU");
+  if (x.get_device() != c10::cuda::current_device()) refuse("tensor must live on the current GPU");
   return x.data_ptr();
 }
 
@@ -53,9 +57,9 @@ void* ptr(PyObject* o) {
     return p;
   }
   const at::Tensor* x = tensor(o, "a tensor, an address or None is wanted");
-  if (!x->is_cuda()) refuse("tensor must live on the GPU");
+  void* p = data(*x);
   if (!x->is_contiguous()) refuse("tensor must be contiguous");
-  return x->data_ptr();
+  return p;
 }
 
 // Several of them, in order (before the stream is asked for: it needs a GPU, and a
