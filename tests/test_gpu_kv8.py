@@ -635,3 +635,134 @@ def test_long_rows_and_many_rows(torch):
                            out, lse, 400)
     assert many.ctx.get_device_error() == 0
     check_rows(many, q, out, lse, range(0, 400, 7), t)
+
+
+# ------------------------------------------------- calls beside each other, repeated
+
+def same_everywhere(torch, c, t, **more):
+    """Buffers and a call of the rows of `t` in any order; returns (call, out, lse)."""
+    q, qd = c.values(len(t), c.hq, c.d, scale=2.0)
+    out = torch.zeros((len(t), c.hq, c.d), dtype=c.kind, device="cuda")
+    lse = torch.zeros((len(t), c.hq), device="cuda")
+    idx, count = listed(c, range(len(t)), len(t))
+    td = c.ints(t)
+    ctx = more.get("ctx", c.ctx)
+
+    def call():
+        ctx.full_attn_kv8(c.fmt, 0, qd, td, c.table, c.codes, c.scales, idx, count, out, lse, len(t))
+    return call, out, lse, q
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,fmt", [(4, 1, 128, "bf16", "int8"), (4, 2, 128, "f32", "e4m3"),
+                                                (4, 1, 64, "bf16", "e4m3"), (2, 2, 128, "bf16", "e4m3")])
+def test_a_context_for_large_batches(torch, hq, hkv, d, dtype, fmt):
+    """A batch of three in a context for 1024 rows, whose row arrays leave room for fewer stages."""
+    c = Case(torch, fmt=fmt, dtype=dtype, hq=hq, hkv=hkv, d=d, rows=3, columns=70)
+    t = [1111, 1, 640]
+    c.write(t, [0] * 3, ring=False)
+    big = c.oda.OdaContext(c.oda.make_config(layers=1, max_batch=1024, hq=hq, hkv=hkv, head_dim=d, sink=4,
+                                             window=32, dtype=dtype, max_blocks_per_seq=70,
+                                             num_blocks=c.blocks))
+    call, out, lse, q = same_everywhere(torch, c, t, ctx=big)
+    call()
+    assert big.get_device_error() == 0
+    check_rows(c, q, out, lse, range(3), t)
+
+
+@pytest.mark.parametrize("fmt,dtype,hq,hkv", [("int8", "bf16", 8, 2), ("e4m3", "f32", 2, 1)])
+def test_equal_calls_give_equal_bits(torch, fmt, dtype, hq, hkv):
+    """Plain, behind other work, from two graphs that share the context's scratch, and while
+    another context works on another stream."""
+    c = Case(torch, fmt=fmt, dtype=dtype, hq=hq, hkv=hkv, rows=4, columns=320)
+    t = [5003, 17, 2048, 901]
+    c.write(t, [0] * 4, ring=False)
+    call, out, lse, q = same_everywhere(torch, c, t)
+    call()
+    check_rows(c, q, out, lse, range(4), t)
+    want = out.clone(), lse.clone()
+    other = Case(torch, fmt=fmt, dtype=dtype, hq=hq, hkv=hkv, rows=2, columns=200, seed=5)
+    t2 = [3001, 3200]
+    other.write(t2, [0, 0], ring=False)
+    call2, out2, lse2, _ = same_everywhere(torch, other, t2)
+    call2()
+    torch.cuda.synchronize()
+    want2 = out2.clone(), lse2.clone()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        out.zero_()
+        out2.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            call()
+            with torch.cuda.stream(side):
+                call2()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(out2, want2[0]) and torch.equal(lse2, want2[1])
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            call()
+            call()
+        graphs.append(g)
+    for _ in range(5):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for g in graphs + graphs[::-1]:
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert c.ctx.get_device_error() == 0 and other.ctx.get_device_error() == 0
+
+
+def test_a_row_listed_twice_and_shared_blocks(torch):
+    """A row twice in the list, and two rows over the same physical blocks (a shared prefix)."""
+    c = Case(torch, fmt="int8", hq=4, hkv=2, rows=3, columns=40)
+    t = [600, 600, 33]
+    c.write(t, [0] * 3, ring=False)
+    c.table[1] = c.table[0]
+    c.table_h[1] = c.table_h[0]
+    q, qd = c.values(3, c.hq, c.d)
+    qd[1] = qd[0]
+    q[1] = q[0]
+    out, lse = torch.zeros((3, c.hq, c.d), dtype=c.kind, device="cuda"), torch.zeros((3, c.hq), device="cuda")
+    idx, count = listed(c, [0, 2, 0], 3)
+    c.ctx.full_attn_kv8("int8", 0, qd, c.ints(t), c.table, c.codes, c.scales, idx, count, out, lse, 3)
+    assert c.ctx.get_device_error() == 0
+    check_rows(c, q, out, lse, [0, 2], t)
+    idx, count = listed(c, [1, 0], 3)
+    c.ctx.full_attn_kv8("int8", 0, qd, c.ints(t), c.table, c.codes, c.scales, idx, count, out, lse, 3)
+    check_rows(c, q, out, lse, [0, 1], t)
+
+
+def test_lists_that_change_between_calls(torch):
+    """Lengths, rows and the block table written by the launch just before, in the same stream:
+    what was worked out ahead of the wait must not be used."""
+    c = Case(torch, fmt="int8", hq=4, hkv=2, rows=4, columns=60)
+    c.write([900, 900, 900, 900], [0] * 4, ring=False)
+    q, qd = c.values(4, c.hq, c.d)
+    out, lse = torch.zeros((4, c.hq, c.d), dtype=c.kind, device="cuda"), torch.zeros((4, c.hq), device="cuda")
+    td, (idx, count) = c.ints([900] * 4), listed(c, range(4), 4)
+    table = c.table.clone()
+    lists = []
+    for _ in range(12):
+        n = int(c.r.integers(1, 5))
+        rows = [int(x) for x in c.r.permutation(4)[:n]]
+        t = [int(x) for x in c.r.integers(1, 901, 4)]
+        perm = c.r.permutation(4)
+        lists.append((rows, t, perm, c.ints(t), *listed(c, rows, 4), c.table[torch.from_numpy(perm).cuda()].contiguous()))
+    got = []
+    for rows, t, perm, t2, i2, n2, tab in lists:               # no wait in between
+        td.copy_(t2)
+        idx.copy_(i2)
+        count.copy_(n2)
+        table.copy_(tab)
+        c.ctx.full_attn_kv8("int8", 0, qd, td, table, c.codes, c.scales, idx, count, out, lse, 4)
+        got.append((out.clone(), lse.clone()))
+    keep = c.table_h.copy()
+    for (rows, t, perm, *_), (o, l) in zip(lists, got):
+        c.table_h = keep[perm]
+        check_rows(c, q, o, l, rows, t)
+    assert c.ctx.get_device_error() == 0
