@@ -11,7 +11,7 @@
 // float64 product's, 2^-53 of the turns).
 //
 // Every element is read once and written once; 16K tokens of 24 heads of 128 (201 MB)
-// take 36 us, 5.6 TB/s, with 77 % of the issue slots in use. Each
+// take 34 us, 5.9 TB/s, with most of the issue slots in use. Each
 // lane owns both elements of its pairs (two 16-byte chunks half a rotated part
 // apart), so the rotation needs no exchange and the norm's sum is one
 // butterfly over the D / 16 lanes (bf16) of a head. A block takes `tok` tokens:
@@ -42,38 +42,38 @@ struct RopeArgs {
   int pos_offset, rot, hq, hkv, tok;
 };
 
-// A chunk as float32 pairs, and back. The arithmetic runs on pairs (packed
-// instructions): with single floats the pass was bound by issuing them.
 template <typename T>
-__device__ __forceinline__ void widen(const uint4 v, float2* x);
+__device__ __forceinline__ void widen(const uint4 v, float* x);
 template <>
-__device__ __forceinline__ void widen<__nv_bfloat16>(const uint4 v, float2* x) {
-  bf16x2_to_f32(v.x, x[0].x, x[0].y);
-  bf16x2_to_f32(v.y, x[1].x, x[1].y);
-  bf16x2_to_f32(v.z, x[2].x, x[2].y);
-  bf16x2_to_f32(v.w, x[3].x, x[3].y);
+__device__ __forceinline__ void widen<__nv_bfloat16>(const uint4 v, float* x) {
+  bf16x2_to_f32(v.x, x[0], x[1]);
+  bf16x2_to_f32(v.y, x[2], x[3]);
+  bf16x2_to_f32(v.z, x[4], x[5]);
+  bf16x2_to_f32(v.w, x[6], x[7]);
 }
 template <>
-__device__ __forceinline__ void widen<float>(const uint4 v, float2* x) {
-  x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-  x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+__device__ __forceinline__ void widen<float>(const uint4 v, float* x) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
 }
 template <typename T>
-__device__ __forceinline__ uint4 narrow(const float2* x);
+__device__ __forceinline__ uint4 narrow(const float* x);
 template <>
-__device__ __forceinline__ uint4 narrow<__nv_bfloat16>(const float2* x) {
+__device__ __forceinline__ uint4 narrow<__nv_bfloat16>(const float* x) {
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 e = __floats2bfloat162_rn(x[i].x, x[i].y);
+    const __nv_bfloat162 e = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     r[i] = *reinterpret_cast<const uint32_t*>(&e);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 template <>
-__device__ __forceinline__ uint4 narrow<float>(const float2* x) {
-  return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
-                    __float_as_uint(x[1].y));
+__device__ __forceinline__ uint4 narrow<float>(const float* x) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3]));
 }
 
 template <typename T, int D, bool NEIGHBOURS, int kThreads>
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   constexpr int EPL = 16 / (int)sizeof(T);          // elements of a chunk
   constexpr int NL = D / EPL / 2;                   // lanes per head, two chunks each
   constexpr int GROUPS = kThreads / NL;
-  // two pairs' cosines and sines in 16 bytes; a lane reads M of them a chunk, stored
+  // (cos, sin) of two pairs in 16 bytes; a lane reads M of them a chunk, stored
   // M apart so that neighbouring lanes read neighbouring 16 bytes
   constexpr int M = NEIGHBOURS ? EPL / 4 : EPL / 2;
   constexpr int UNITS = D / 4;
@@ -130,36 +130,32 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         const double turns = pos * ((double)a.inv_freq[f] * 0.15915494309189533577);
         float s, c;
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-        float* unit = reinterpret_cast<float*>(&turn[t][slot(f / 2)]);
-        unit[f & 1] = c;
-        unit[2 + (f & 1)] = s;
+        reinterpret_cast<float2*>(&turn[t][slot(f / 2)])[f & 1] = make_float2(c, s);
       }
       __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-      float2 x[2][EPL / 2];
+      float x[2][EPL];
       widen<T>(v[u][0], x[0]);
       widen<T>(v[u][1], x[1]);
       const bool is_k = ih[u] >= a.hq;
       const T* w = static_cast<const T*>(is_k ? a.k_weight : a.q_weight);
       // (every lane reduces: a warp may hold heads with a weight and without, or none)
-      float2 sq = make_float2(0.f, 0.f);
+      float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL / 2; ++i) sq = __ffma2_rn(x[0][i], x[0][i], __ffma2_rn(x[1][i], x[1][i], sq));
-      float ss = sq.x + sq.y;
+      for (int i = 0; i < EPL; ++i) ss = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], ss));
 #pragma unroll
       for (int o = 1; o < NL; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, NL);
       if (itk[u] >= ntok) continue;
       if (w) {
-        const float r1 = rsqrtf(ss * (1.f / D) + a.eps);
-        const float2 r = make_float2(r1, r1);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          float2 wf[EPL / 2];
+          float wf[EPL];
           widen<T>(*reinterpret_cast<const uint4*>(w + (p ? c1 : c0)), wf);
 #pragma unroll
-          for (int i = 0; i < EPL / 2; ++i) x[p][i] = __fmul2_rn(__fmul2_rn(x[p][i], r), wf[i]);
+          for (int i = 0; i < EPL; ++i) x[p][i] = x[p][i] * r * wf[i];
         }
       }
       if (rotated) {
@@ -171,20 +167,23 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 #pragma unroll
             for (int m = 0; m < M; ++m) {
               const float4 cs = tt[slot(u0 + m)];
-              const float2 y0 = x[p][2 * m], y1 = x[p][2 * m + 1];
-              x[p][2 * m] = make_float2(y0.x * cs.x - y0.y * cs.z, y0.y * cs.x + y0.x * cs.z);
-              x[p][2 * m + 1] = make_float2(y1.x * cs.y - y1.y * cs.w, y1.y * cs.y + y1.x * cs.w);
+              float* y = x[p] + 4 * m;
+              const float y0 = y[0], y1 = y[1], y2 = y[2], y3 = y[3];
+              y[0] = y0 * cs.x - y1 * cs.y;
+              y[1] = y1 * cs.x + y0 * cs.y;
+              y[2] = y2 * cs.z - y3 * cs.w;
+              y[3] = y3 * cs.z + y2 * cs.w;
             }
           }
         } else {
-          const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
           for (int m = 0; m < M; ++m) {
             const float4 cs = tt[slot(li * M + m)];
-            const float2 c = make_float2(cs.x, cs.y), s = make_float2(cs.z, cs.w);
-            const float2 a2 = x[0][m], b2 = x[1][m];
-            x[0][m] = __ffma2_rn(minus, __fmul2_rn(b2, s), __fmul2_rn(a2, c));
-            x[1][m] = __ffma2_rn(a2, s, __fmul2_rn(b2, c));
+            const float a0 = x[0][2 * m], a1 = x[0][2 * m + 1], b0 = x[1][2 * m], b1 = x[1][2 * m + 1];
+            x[0][2 * m] = a0 * cs.x - b0 * cs.y;
+            x[1][2 * m] = b0 * cs.x + a0 * cs.y;
+            x[0][2 * m + 1] = a1 * cs.z - b1 * cs.w;
+            x[1][2 * m + 1] = b1 * cs.z + a1 * cs.w;
           }
         }
       }
@@ -200,9 +199,10 @@ template <typename T, int D, int kThreads>
 oda_status launch_threads(RopeArgs& a, bool neighbours, int sms, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D * (int)sizeof(T) / 32);
   const int heads = a.hq + (a.k ? a.hkv : 0);
-  // as many tokens a block as its lanes hold at once, while every SM has a block
-  // (1537 tokens of 6 heads: 3.0 us; with four blocks for every SM 4.2)
-  a.tok = kItems * GROUPS / heads;
+  // twice the tokens that a block's lanes hold at once (16K tokens of 24 heads: 34.2 us;
+  // once 35.7, three times 36.5), while every SM has a block (1537 tokens of 6
+  // heads: 3.0 us; with four blocks for every SM 4.2)
+  a.tok = 2 * kItems * GROUPS / heads;
   a.tok = a.tok < 1 ? 1 : a.tok > kMaxTok ? kMaxTok : a.tok;
   while (a.tok > 1 && ceil_div64(a.n, a.tok) < sms) --a.tok;
   const long long grid = ceil_div64(a.n, a.tok);
@@ -214,7 +214,7 @@ oda_status launch_threads(RopeArgs& a, bool neighbours, int sms, cudaStream_t st
 
 // Fewer tokens than SMs: a block has an SM to itself, the larger one is quicker
 // (16 tokens of 24 heads: 2.2 against 2.6 us). More: smaller blocks leave fewer
-// loads waiting for a block's last (16K tokens: 36.0 against 37.0 us).
+// loads waiting for a block's last (16K tokens, once: 36.0 against 37.0 us).
 template <typename T, int D>
 oda_status launch_td(RopeArgs& a, bool neighbours, int sms, cudaStream_t st) {
   return a.n < sms ? launch_threads<T, D, 256>(a, neighbours, sms, st)
