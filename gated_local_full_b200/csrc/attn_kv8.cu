@@ -36,9 +36,12 @@
 //   * K (first operand): chunks tg and tg + 4 (d = 128) of the lane's two tokens.
 //   * V (first operand, 16 dims x 16 tokens): D / 8 dims of tokens 4 tg .. 4 tg + 3,
 //     the tokens in rows 2 tg, 2 tg + 1, 2 tg + 8, 2 tg + 9. The eight lanes that
-//     shared memory serves together read four tokens, four rows apart: each four
-//     rows of V are a copy of their own, 32 bytes further than they would be,
-//     so that the lanes meet in no bank.
+//     shared memory serves together read four tokens, four rows apart, at the
+//     same 32 bytes of their rows: V's second half is a copy of its own, 64
+//     bytes further than it would be, so that no more than two lanes meet in a
+//     bank. (Tiles in one copy, two and four, the last with no two lanes in a
+//     bank: 8 rows of 16K tokens 49.2, 48.2 and 50.8 us, the mixed batch 188, 187
+//     and 195: the copy engine's time against shared memory's.)
 //
 // Bound by HBM for long rows (one of 128K tokens, 8 KV heads, d = 128: 48.8 us
 // for 270 MB, 5.5 TB/s with the start and the merge; 15 rows of 4K to 64K: 184 us,
@@ -52,7 +55,10 @@ using namespace oda;
 namespace {
 
 constexpr int W = 6;                     // warps per CTA
-constexpr int kBatch = 4;                // pairs of tiles of a warp looked up together, eight lanes each
+constexpr int kCopies = 2;               // copies of a tile, a lane each (above)
+constexpr int kRows = 16 / kCopies;      // rows of V of each
+constexpr int kSkew = 128 / kCopies;     // bytes that each lies further than it would
+constexpr int kBatch = 16 / kCopies;     // pairs of tiles of a warp looked up together
 constexpr int kAhead = 16;               // tiles of a CTA put into L2 before the dependency wait
 constexpr float kNone = -3.402823466e38f;  // a reference before any token: no finite score is below
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per barrier wait
@@ -173,9 +179,9 @@ struct Tile {
   static constexpr int KC = D / 64;      // chunks of K per lane and column
   static constexpr int VW = D / 32;      // 32-bit words of V per token and lane
   static constexpr int MT = D / 16;      // 16-dim slices of the output
-  static constexpr int VG = 4 * D + 32;  // V's pitch of four tokens in a stage
+  static constexpr int VG = kRows * D + kSkew;  // V's pitch of a copy's rows in a stage
   static constexpr int BYTES = 2 * ODA_TILE * D;               // in the cache
-  static constexpr int STAGE = ODA_TILE * D + 4 * VG;          // in shared memory
+  static constexpr int STAGE = ODA_TILE * D + kCopies * VG;    // in shared memory
 };
 
 constexpr float kLift = 11.f;            // weights are at most 2^15 < 65504
@@ -654,7 +660,7 @@ __device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo,
 // a time are two independent chains of arithmetic: one alone left a warp waiting
 // for its own results two cycles of three (128K tokens: 57 us with 8 warps of one
 // tile at a time, 52 with 6 warps of two). What a copy needs is worked out for
-// kBatch pairs at once, eight lanes a pair, one for each of its copies; the block ids
+// kBatch pairs at once, four lanes a pair, one for each of its copies; the block ids
 // are looked up a batch ahead. (Tile by tile this cost as many instructions as
 // the arithmetic.) Which tile a warp takes depends on the lists alone, so equal
 // calls give equal bits.
@@ -724,15 +730,15 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   }
 
   // ---- copies
-  const int tile = (lane >> 2) & 1, piece = lane & 3;        // this lane's copy of its pair
+  const int tile = (lane / kCopies) & 1, piece = lane % kCopies;   // this lane's copy of its pair
   const uint64_t policy = l2_policy_evict_first();           // K/V is read once a launch
   const unsigned char* stages = smem + (uint32_t)(warp * ns * 2 * STAGE);
   Meta* meta = reinterpret_cast<Meta*>(smem + lay.meta) + warp * ns * 2;
   const uint32_t to = smem_addr(stages) + tile * STAGE + (piece ? ODA_TILE * D + piece * Tile<D>::VG : 0);
-  const uint32_t from = piece ? ODA_TILE * D + piece * 4 * D : 0;
-  const uint32_t bytes = piece ? 4 * D : (ODA_TILE + 4) * D; // K and V's first four tokens; four of V
+  const uint32_t from = piece ? ODA_TILE * D + piece * kRows * D : 0;
+  const uint32_t bytes = (piece ? kRows : ODA_TILE + kRows) * D;   // the first: K too
   Walk at;
-  int pair = warp + W * (lane >> 3), blk = -1, jt = 0;       // of the next batch
+  int pair = warp + W * (lane / (2 * kCopies)), blk = -1, jt = 0;       // of the next batch
   bool there;
   auto lookup = [&]() {
     there = at.seek(rowstart, a.hkv, hi, pair);
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       pair += W * kBatch;
       lookup();
     }
-    if ((lane >> 3) == issued % kBatch) {
+    if (lane / (2 * kCopies) == issued % kBatch) {
       const uint32_t bar = full + 8 * islot;
       if (piece == 0) {
         Meta& mt = meta[2 * islot + tile];
@@ -803,7 +809,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   float* pml = a.partials + (size_t)a.max_parts * G * D;
   const int lg = lane >> 2, tg = lane & 3;
   const uint32_t k_at = (4 * (lg >> 1) + (lg & 1)) * D + tg * 16;
-  const uint32_t v_at = ODA_TILE * D + tg * Tile<D>::VG + lg * (D / 8);
+  const uint32_t v_at = ODA_TILE * D + tg * 4 * D + tg * 4 / kRows * kSkew + lg * (D / 8);
   int slot = 0, used = 0;
   uint32_t parity = 0;
   bool aborted = false;
