@@ -13,7 +13,7 @@
 //     one wave; bound by the latency of lengths -> block id -> scale (28 layers of 32
 //     rows, 8 KV heads: 5 us).
 //   append, any number: a warp a unit, the new tokens requested before the
-//     block id; issue slots (65 %) and HBM bind it (16K tokens, 100 MB: 17 us).
+//     block id; bound by HBM (16K tokens, 100 MB: about 17 us).
 //   read: a warp takes kReadUnits units of an item, whose codes are all
 //     requested before the first is turned into values: half of the item
 //     numbers may be empty, and finding an item costs two round trips. Bound by
