@@ -766,3 +766,58 @@ def test_lists_that_change_between_calls(torch):
         c.table_h = keep[perm]
         check_rows(c, q, o, l, rows, t)
     assert c.ctx.get_device_error() == 0
+
+
+def test_refusals_of_the_compiled_calls(torch):
+    """What the binding itself refuses, and what it hands on: nothing is launched."""
+    c = Case(torch, rows=2, columns=2)
+    oda = c.oda
+    t, idx = c.ints([3, 4]), listed(c, [0, 1], 2)
+    (_, kd), (_, vd) = c.values(1, 2, c.hkv, c.d), c.values(1, 2, c.hkv, c.d)
+    _, qd = c.values(2, c.hq, c.d)
+    out = torch.zeros_like(qd)
+
+    def append(format="int8", k=kd, v=vd, sl=t, B=2, stream=None):
+        c.ctx.append_kv8(format, 0, 1, k, v, sl, c.table, c.codes, c.scales, None, B, stream=stream)
+
+    def attn(ctx=c.ctx, format="int8", q=qd, table=c.table, out=out, stream=None):
+        ctx.full_attn_kv8(format, 0, q, t, table, c.codes, c.scales, *idx, out, None, 2, stream=stream)
+
+    for f in (append, attn):
+        for name in ("int3", 0, 9):
+            with pytest.raises(oda.OdaError) as e:
+                f(format=name)
+            assert e.value.status == oda.ERR_DTYPE
+        with pytest.raises(TypeError):
+            f(format=None)
+        with pytest.raises((AttributeError, TypeError, ValueError)):
+            f(stream="s")
+    with pytest.raises(ValueError, match="tensor"):
+        append(k=[1.0])
+    with pytest.raises(ValueError, match="tensor"):
+        append(k=None)
+    with pytest.raises(ValueError, match="contiguous"):
+        append(k=kd.expand(1, 2, c.hkv, c.d).transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(ValueError, match="GPU"):
+        append(sl=t.cpu())
+    with pytest.raises(ValueError, match="contiguous"):
+        attn(table=c.table.t())
+    with pytest.raises(oda.OdaError) as e:
+        attn(q=None)
+    assert e.value.status == oda.ERR_ARG
+    with pytest.raises(TypeError):
+        append(B="two")
+    gone = oda.OdaContext(c.cfg)
+    attn(ctx=gone)
+    torch.cuda.synchronize()
+    gone.close()
+    with pytest.raises(oda.OdaError) as e:
+        attn(ctx=gone)
+    assert e.value.status == oda.ERR_ARG
+    # addresses in tensors' place, and streams as objects and numbers
+    s = torch.cuda.Stream()
+    for x in (s, s.cuda_stream, None):
+        c.ctx.full_attn_kv8(oda.KV8_INT8, 0, qd.data_ptr(), t.data_ptr(), c.table, c.codes, c.scales, *idx,
+                            out.data_ptr(), 0, 2, stream=x)
+    torch.cuda.synchronize()
+    assert c.ctx.get_device_error() == 0
