@@ -46,6 +46,8 @@
 // Bound by HBM for long rows (one of 128K tokens, 8 KV heads, d = 128: 48.8 us
 // for 270 MB, 5.5 TB/s with the start and the merge; 15 rows of 4K to 64K: 184 us,
 // 6.3 TB/s), by latency for short ones (two rows of 64: 4.2 us).
+#define ODA_PLAN_ROLLED
+
 #include "kv8.cuh"
 #include "plan.cuh"
 #include "tiles.cuh"
@@ -186,16 +188,17 @@ struct Tile {
 
 constexpr float kLift = 11.f;            // weights are at most 2^15 < 65504
 
-// The head of a lane's scores, of a segment's up to two or four.
+// The head of a lane's scores: of up to two a segment, or (wide) of up to four.
 __device__ __forceinline__ int head_of(int tg, bool wide) { return (tg >> 1) + (wide ? 2 * (tg & 1) : 0); }
 
 // A warp's running state for one segment (row, KV head).
-template <typename T, int D, int FMT>
+template <typename T, int D, int FMT, bool WIDE>
 struct State {
   static constexpr int KC = Tile<D>::KC;
+  static constexpr int SETS = WIDE ? 2 : 1;   // int8: of digit columns, two heads each
   // second operand of the scores: products (int8: of two words, a set for two
   // heads; e4m3: of one word)
-  uint32_t qf[4 * KC][2];
+  uint32_t qf[FMT == kInt8 ? 2 * KC * SETS : 4 * KC][2];
   float qs;                              // this lane's head: what its sums count for, times the scores' scale
   float m, M, l, K;                      // K = 2^(m - M + kLift), infinite while M is kNone
   float acc[Tile<D>::MT][4];             // [0] + [1]: one dim of this lane's head, [2] + [3]: the next
@@ -212,15 +215,14 @@ struct State {
 
   // The elements that this lane's columns need, asked for before they are wanted.
   struct Query {
-    static constexpr int SETS = FMT == kInt8 ? 2 : 1;
+    static constexpr int SETS = FMT == kInt8 ? State::SETS : 1;
     uint4 r[SETS][KC][sizeof(T)];
     // q: the G query heads of the segment, [G][D]
     __device__ __forceinline__ void fetch(const T* q, int G, int lane) {
       const int g = lane >> 2, tg = lane & 3;
-      const bool wide = G > 2;
 #pragma unroll
       for (int set = 0; set < SETS; ++set) {
-        const int h = FMT == kInt8 ? 2 * set + (g >> 2) : head_of(g >> 1, wide);
+        const int h = FMT == kInt8 ? 2 * set + (g >> 2) : head_of(g >> 1, WIDE);
 #pragma unroll
         for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -256,15 +258,11 @@ struct State {
 
   __device__ __forceinline__ void set_q(const Query& q, int G, float qscale, int lane) {
     const int g = lane >> 2, tg = lane & 3;
-    const bool wide = G > 2;
     float x[KC][16];
     if constexpr (FMT == kInt8) {        // column g: digit g % 4 of head g / 4, and of head 2 + g / 4
 #pragma unroll
-      for (int p = 0; p < 4 * KC; ++p) qf[p][0] = qf[p][1] = 0u;
-#pragma unroll
-      for (int set = 0; set < 2; ++set) {
-        if (set == 1 && !wide) break;
-        const float up = scale_head(q.r[set % Query::SETS], 29, x);
+      for (int set = 0; set < SETS; ++set) {
+        const float up = scale_head(q.r[set], 29, x);
         // y = d0 + 256 d1 + 256^2 d2 + 256^3 d3, each within -128 .. 127: digit k is byte k of
         // y plus half of what the digits below it can hold
         const int k = g & 3;
@@ -305,7 +303,7 @@ struct State {
 
   // The scores of this lane's head with the tokens in rows g and g + 8, before the block's scale.
   // (p_k: this lane's place in the stage's K)
-  __device__ __forceinline__ void scores(float (&s)[2], const unsigned char* p_k, bool wide, int tg) const {
+  __device__ __forceinline__ void scores(float (&s)[2], const unsigned char* p_k, int tg) const {
     uint32_t k[2][KC][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -317,10 +315,9 @@ struct State {
     if constexpr (FMT == kInt8) {
       // |sum| <= 2^21: the accumulators start at the bits of 1.5 * 2^23, and are floats as they stand
       const float f = tg & 1 ? 65536.f : 1.f;
-      float v[2][2];
+      float v[SETS][2];
 #pragma unroll
-      for (int set = 0; set < 2; ++set) {
-        if (set == 1 && !wide) break;
+      for (int set = 0; set < SETS; ++set) {
         int c[4] = {0x4b400000, 0x4b400000, 0x4b400000, 0x4b400000};
 #pragma unroll
         for (int p = 0; p < 2 * KC; ++p)
@@ -335,8 +332,8 @@ struct State {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float keep = v[0][i], send = v[0][i];
-        if (wide) {
-          if (tg & 1) keep = v[1][i]; else send = v[1][i];
+        if (WIDE) {
+          if (tg & 1) keep = v[SETS - 1][i]; else send = v[SETS - 1][i];
         }
         s[i] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
       }
@@ -445,12 +442,11 @@ struct State {
   // This warp's (acc, M, m, l) for every head: ws [G][D + 4].
   __device__ __forceinline__ void store(float* ws, int G, int lane) {
     const int g = lane >> 2, tg = lane & 3;
-    const bool wide = G > 2;
     l += __shfl_xor_sync(0xffffffffu, l, 4);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
-    const int h = head_of(tg, wide);
-    if (h >= G || (!wide && (tg & 1))) return;
+    const int h = head_of(tg, WIDE);
+    if (h >= G || (!WIDE && (tg & 1))) return;
     float* w = ws + h * (D + 4);
 #pragma unroll
     for (int i = 0; i < Tile<D>::MT; ++i) {
@@ -676,7 +672,7 @@ __device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo,
 // calls give equal bits. Loops that are not unrolled for their arrays are kept
 // rolled: fetching instructions is a quarter of a warp's time (a row of 700
 // tokens 9.7 -> 9.4 us, 32 rows of 1500 20.5 -> 20.1).
-template <typename T, int D, int FMT>
+template <typename T, int D, int FMT, bool WIDE>
 __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) {
   constexpr int TILE = Tile<D>::BYTES, STAGE = Tile<D>::STAGE;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -696,23 +692,23 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
   if (lane < ns) mbar_init(full + 8 * lane, 4);              // the codes' bytes and the scales of two tiles
   fence_mbar_init();
-  bool guessed = false;
-  if (!a.early) {
+  if (warp == 0) {
     // Before the dependency wait: the partition from lists that the launch before may
     // still be writing (every value is checked before it is used as an index), and
     // this CTA's first tiles into L2. A prefetch reads no value, and after the wait
     // the lists are compared, so a stale guess costs only time.
-    // (A CTA that started late, the wait already over, leaves the prefetch out.)
-    if (warp == 1) {
-      if (lane == 0) *const_cast<volatile int*>(&waited) = 0;
-      pdl_wait();
-      if (lane == 0) *const_cast<volatile int*>(&waited) = 1;
-    }
-    if (warp == 0) {
-      partition(a, false, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
-      guessed = true;
+    // (One loop for the guess and the partition proper: their code is large.)
+#pragma unroll 1
+    for (int pass = a.early ? 1 : 0; pass < 2; ++pass) {
+      if (pass == 1 && !a.early) {
+        pdl_wait();
+        pdl_launch_dependents();
+        if (same_lists(a, sinfo, rowb, rowt, rowlo)) break;
+      }
+      partition(a, pass == 1, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
       const int k = sinfo[4] + lane;
-      if (!*const_cast<volatile int*>(&waited) && sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
+      // (a CTA that started late, the wait already over, leaves the prefetch out)
+      if (pass == 0 && !*const_cast<volatile int*>(&waited) && sinfo[0] > 0 && k < sinfo[5] && lane < kAhead) {
         Cursor c;
         locate(rowstart, sinfo[0], a.hkv, k, c);
         const int col = (rowlo[c.i] - 1) / ODA_TILE + k - (c.s1 - c.nt);
@@ -725,11 +721,12 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       }
       __syncwarp();
     }
+  } else if (!a.early) {
+    if (tid == 32) *const_cast<volatile int*>(&waited) = 0;
     pdl_wait();
     pdl_launch_dependents();
+    if (tid == 32) *const_cast<volatile int*>(&waited) = 1;
   }
-  if (warp == 0 && !(guessed && same_lists(a, sinfo, rowb, rowt, rowlo)))
-    partition(a, true, sinfo, &swalk, rowb, rowt, rowstart, rowcs, rowlo);
   __syncthreads();
   const int nr = sinfo[0], total = sinfo[1], P = sinfo[2], aligned = sinfo[3];
   const int lo = sinfo[4], hi = sinfo[5];
@@ -764,7 +761,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   const int count = (sinfo[9] - warp + W - 1) / W;           // this warp's pairs
   Walk seg = swalk;
   const int hq = a.hkv * G;
-  typename State<T, D, FMT>::Query query;
+  typename State<T, D, FMT, WIDE>::Query query;
   auto fetch = [&]() {
     query.fetch(static_cast<const T*>(a.q) + ((long long)rowb[seg.i] * hq + seg.g * G) * D, G, lane);
   };
@@ -829,7 +826,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
 #pragma unroll 1
   while (true) {
     const int b = rowb[seg.i], g = seg.g, s0 = seg.s1 - seg.nt, s1 = seg.s1;
-    State<T, D, FMT> st;
+    State<T, D, FMT, WIDE> st;
     st.reset();
     st.set_q(query, G, a.qscale, lane);
 #pragma unroll 1
@@ -839,16 +836,14 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         aborted = true;
         break;
       }
-      int wide = G > 2;
-      asm volatile("" : "+r"(wide));                          // one loop for both, not two
       const Meta ma = meta[2 * slot], mb = meta[2 * slot + 1];
       const unsigned char* stage = stages + (uint32_t)(slot * 2 * STAGE);
       const uint32_t masks[2] = {ma.mask, mb.mask};
       const float2 scales[2] = {ma.scale, mb.scale};
       float raw[2][2];
       uint32_t w[2][2], v[2][4][Tile<D>::VW];
-      st.scores(raw[0], stage + k_at, wide != 0, tg);
-      st.scores(raw[1], stage + STAGE + k_at, wide != 0, tg);
+      st.scores(raw[0], stage + k_at, tg);
+      st.scores(raw[1], stage + STAGE + k_at, tg);
       load_v<D>(v[0], stage + v_at, masks[0], lane);
       load_v<D>(v[1], stage + STAGE + v_at, masks[1], lane);
       __syncwarp();                                          // every lane has its share
@@ -950,8 +945,10 @@ size_t smem_bytes(const oda_config& c) {
 
 template <typename F>
 oda_status dispatch(const oda_config& c, int format, F&& f) {
-#define ODA_CASE(TT, DT, DD, FF)                                     \
-  if (c.dtype == DT && c.head_dim == DD && format == FF) return f.template operator()<TT, DD, FF>();
+  const bool wide = c.hq / c.hkv > 2;
+#define ODA_CASE(TT, DT, DD, FF)                                                   \
+  if (c.dtype == DT && c.head_dim == DD && format == FF)                           \
+    return wide ? f.template operator()<TT, DD, FF, true>() : f.template operator()<TT, DD, FF, false>();
   ODA_CASE(__nv_bfloat16, ODA_BF16, 128, kInt8) ODA_CASE(__nv_bfloat16, ODA_BF16, 128, kE4m3)
   ODA_CASE(__nv_bfloat16, ODA_BF16, 64, kInt8) ODA_CASE(__nv_bfloat16, ODA_BF16, 64, kE4m3)
   ODA_CASE(float, ODA_F32, 128, kInt8) ODA_CASE(float, ODA_F32, 128, kE4m3)
@@ -963,9 +960,9 @@ oda_status dispatch(const oda_config& c, int format, F&& f) {
 struct Setup {
   oda_ctx* ctx;
   int* ctas;
-  template <typename T, int D, int FMT>
+  template <typename T, int D, int FMT, bool WIDE>
   oda_status operator()() {
-    const void* k = reinterpret_cast<const void*>(attn_kv8_kernel<T, D, FMT>);
+    const void* k = reinterpret_cast<const void*>(attn_kv8_kernel<T, D, FMT, WIDE>);
     const size_t sm = smem_bytes(ctx->cfg);
     ODA_CUDA_TRY(raise_smem_limit(k, sm));
     int occ = 0;
@@ -980,9 +977,9 @@ struct Launch {
   oda_ctx* ctx;
   const Attn8Args* a;
   cudaStream_t st;
-  template <typename T, int D, int FMT>
+  template <typename T, int D, int FMT, bool WIDE>
   oda_status operator()() {
-    return launch_pdl(attn_kv8_kernel<T, D, FMT>, dim3(ctx->attn_kv8_ctas), dim3(W * 32),
+    return launch_pdl(attn_kv8_kernel<T, D, FMT, WIDE>, dim3(ctx->attn_kv8_ctas), dim3(W * 32),
                       smem_bytes(ctx->cfg), st, *a) == cudaSuccess
                ? ODA_OK
                : ODA_ERR_CUDA;

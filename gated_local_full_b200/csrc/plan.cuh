@@ -23,6 +23,14 @@
 
 #include "oda_internal.cuh"
 
+// A file that wants small code more than an unrolled partition (for more rows than a
+// warp has lanes) defines ODA_PLAN_ROLLED.
+#ifdef ODA_PLAN_ROLLED
+#define ODA_PLAN_LOOP _Pragma("unroll 1")
+#else
+#define ODA_PLAN_LOOP
+#endif
+
 namespace oda {
 
 struct PlanIn {
@@ -66,6 +74,7 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
     }
   }
   int carry = 0;
+  ODA_PLAN_LOOP
   for (int base = 0; base < nr; base += 32) {
     const int i = base + lane;
     int nt = 0;
@@ -113,6 +122,7 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
   if (tot > 0) P = min(P, max(1, (tot + p.min_tiles - 1) / p.min_tiles));
   // per-row CTA counts of the aligned partition, their prefix, the worst load
   int carry2 = 0, worst = 0;
+  ODA_PLAN_LOOP
   for (int base = 0; base < nr; base += 32) {
     const int i = base + lane;
     int n = 0;
@@ -159,6 +169,7 @@ __device__ __forceinline__ void plan_cta(int cta, const PlanHead& h, const int* 
   if (h.al) {
     if (cta >= rowcs[h.nr]) return;
     int r0 = 0, r1 = h.nr - 1;                   // row with rowcs[r0] <= cta < rowcs[r0+1]
+    ODA_PLAN_LOOP
     while (r0 < r1) {
       const int mid = (r0 + r1 + 1) >> 1;
       if (rowcs[mid] <= cta) r0 = mid; else r1 = mid - 1;
