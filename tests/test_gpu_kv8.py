@@ -821,3 +821,44 @@ def test_refusals_of_the_compiled_calls(torch):
                             out.data_ptr(), 0, 2, stream=x)
     torch.cuda.synchronize()
     assert c.ctx.get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt,dtype,hq,hkv,d", [("int8", "bf16", 4, 2, 128), ("e4m3", "bf16", 4, 1, 128),
+                                                ("int8", "f32", 4, 1, 64), ("e4m3", "f32", 2, 2, 128)])
+def test_inputs_ready(torch, fmt, dtype, hq, hkv, d):
+    """The first tiles staged before the dependency wait: the same bits, with new queries written
+    by the launch just before, for rows of all lengths, regions, and no rows."""
+    c = Case(torch, fmt=fmt, dtype=dtype, hq=hq, hkv=hkv, d=d, rows=5, columns=130)
+    t = [2077, 1, 16, 515, 1300]
+    c.write(t, [0] * 5, ring=False)
+    lo, hi = [3, 1, 2, 200, 1000], [2078, 2, 17, 201, 1299]
+    qs = [c.values(5, hq, d, scale=2.0) for _ in range(4)]
+    qd = torch.zeros_like(qs[0][1])
+    td, ld, hd = c.ints(t), c.ints(lo), c.ints(hi)
+
+    def run(ready, region, rows):
+        idx, count = listed(c, rows, 5)
+        got = []
+        torch.cuda.synchronize()
+        for _, q in qs:
+            out = torch.full_like(qd, 7.0)
+            lse = torch.full((5, hq), 7.0, device="cuda")
+            qd.copy_(q)
+            if region:
+                c.ctx.range_attn_kv8(fmt, 0, qd, td, ld, hd, c.table, c.codes, c.scales, idx, count, out, lse,
+                                     5, inputs_ready=ready)
+            else:
+                c.ctx.full_attn_kv8(fmt, 0, qd, td, c.table, c.codes, c.scales, idx, count, out, lse, 5,
+                                    inputs_ready=ready)
+            got.append((out, lse))
+        torch.cuda.synchronize()
+        assert c.ctx.get_device_error() == 0
+        return got
+
+    for region in (False, True):
+        for rows in ([0, 1, 2, 3, 4], [4, 1], [2], []):
+            plain, early = run(False, region, rows), run(True, region, rows)
+            for (o, l), (o2, l2) in zip(plain, early):
+                assert torch.equal(o, o2) and torch.equal(l, l2)
+            for (q, _), (o, l) in zip(qs, early):
+                check_rows(c, q, o, l, rows, t, *((lo, hi) if region else ()))
