@@ -53,7 +53,8 @@ struct PlanHead {
 };
 
 // Warp 0 only. Writes rowb/rowt [nr], rowstart/rowcs [nr+1], and for the
-// paged source rowlo [nr] (the region's first position; rowt is its last).
+// paged source rowlo [nr] (the region's first position; rowt is its last; both
+// 0 for a row that is refused).
 __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* rowt,
                                               int* rowstart, int* rowcs, int* rowlo = nullptr) {
   const int lane = threadIdx.x & 31;
@@ -103,6 +104,9 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
           nt = tend - (first - 1) / ODA_TILE;
         }
       }
+      // a refused row holds no position: whoever compares the lists with what a partition was
+      // worked out from must not find its bounds unchanged (the length may be what has changed)
+      if (nt == 0) first = last = 0;
       rowb[i] = okl ? bl : 0;
       rowt[i] = ring ? t : last;
       if (rowlo) rowlo[i] = first;

@@ -862,3 +862,79 @@ def test_inputs_ready(torch, fmt, dtype, hq, hkv, d):
                 assert torch.equal(o, o2) and torch.equal(l, l2)
             for (q, _), (o, l) in zip(qs, early):
                 check_rows(c, q, o, l, rows, t, *((lo, hi) if region else ()))
+
+
+# ------------------------------------------------- lists written late by the launch before
+
+@pytest.fixture(scope="module")
+def late_store(tmp_path_factory):
+    """late_store(dst, src): a launch that releases the next one before it stores dst."""
+    import ctypes
+    import os
+    import subprocess
+
+    from gated_local_full_b200 import build
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "late_store.cu")
+    lib = str(tmp_path_factory.mktemp("late") / "late_store.so")
+    r = subprocess.run([build.nvcc(), *build.ARCH, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", src,
+                        "-o", lib], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    f = ctypes.CDLL(lib).late_store
+    f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p]
+
+    def store(dst, new):
+        import torch
+        assert dst.numel() == new.numel() and dst.dtype == new.dtype == torch.int32
+        assert f(dst.data_ptr(), new.data_ptr(), new.numel(), 60000,
+                 torch.cuda.current_stream().cuda_stream) == 0
+    return store
+
+
+@pytest.mark.parametrize("late,region", [(k, False) for k in ("t", "idx", "count", "table")] +
+                         [(k, True) for k in ("t", "idx", "count", "lo", "hi", "table")])
+def test_a_list_written_late_by_the_launch_before(torch, late_store, late, region):
+    """The launch before lets the attention start, and only then stores one of the lists: lengths
+    that a region's end outgrows or that are refused as they were, ids and blocks out of range, counts
+    of none and of too many, bounds of nothing. What was worked out from the old list must not be used, and
+    the call after it, with nothing changed, gives the same bits (no ticket is left over)."""
+    c = Case(torch, fmt="int8", hq=4, hkv=2, rows=5, columns=130)
+    full_t = [2077, 900, 16, 515, 1300]
+    c.write(full_t, [0] * 5, ring=False)
+    q, qd = c.values(5, c.hq, c.d)
+    held = {k: c.ints([0] * (1 if k == "count" else 5)) for k in ("t", "idx", "count", "lo", "hi")}
+    held["table"] = c.table.flatten()
+    blocks = c.table_h.reshape(-1).tolist()
+    for step in range(10):
+        t = [int(c.r.integers(x // 2 + 1, x + 1)) for x in full_t]
+        rows = [int(x) for x in c.r.permutation(5)[:1 + step % 5]]
+        hi = [x + 1 for x in t]                            # regions that end at the row's last position
+        lo = [int(c.r.integers(1, h)) for h in hi]
+        new = dict(t=t, idx=rows + [-1] * (5 - len(rows)), count=[len(rows)], lo=lo, hi=hi, table=blocks)
+        old = dict(t=[[1] * 5, [x - 1 for x in t], [0] * 5, [x // 3 + 1 for x in t], [2 ** 31 - 1] * 5],
+                   idx=[[-1] * 5, [4, 3, 2, 1, 0], [7] * 5, [0] * 5, [2 ** 31 - 1] * 5],
+                   count=[[0], [5], [9], [-3], [1]],
+                   lo=[[0] * 5, [x + 1 for x in t], [1] * 5, [-5] * 5, [x // 2 for x in hi]],
+                   hi=[[0] * 5, [x + 1 for x in lo], [x + 2 for x in t], [-2 ** 31] * 5, [x // 2 + 1 for x in hi]],
+                   table=[blocks[::-1], [-1] * 650, [c.blocks] * 650, [0] * 650, blocks[130:] + blocks[:130]])
+        before = old[late][step % 5]
+        device = {k: c.ints(v) for k, v in new.items()}
+        for k in held:
+            held[k].copy_(c.ints(before) if k == late else device[k])
+        out = torch.full((5, c.hq, c.d), 7.0, dtype=c.kind, device="cuda")
+        lse = torch.full((5, c.hq), 7.0, device="cuda")
+        again, lse2 = out.clone(), lse.clone()
+        torch.cuda.synchronize()
+        late_store(held[late], device[late])
+        for o, l in ((out, lse), (again, lse2)):
+            table = held["table"].view(5, 130)
+            if region:
+                c.ctx.range_attn_kv8(c.fmt, 0, qd, held["t"], held["lo"], held["hi"], table, c.codes, c.scales,
+                                     held["idx"], held["count"], o, l, 5)
+            else:
+                c.ctx.full_attn_kv8(c.fmt, 0, qd, held["t"], table, c.codes, c.scales, held["idx"],
+                                    held["count"], o, l, 5)
+        assert c.ctx.get_device_error() == 0, step
+        check_rows(c, q, out, lse, rows, t, *((lo, hi) if region else ()))
+        assert torch.equal(out, again) and torch.equal(lse, lse2), (step, before)
+        rest = [b for b in range(5) if b not in rows]
+        assert (out[rest] == 7).all()
