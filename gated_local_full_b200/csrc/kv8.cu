@@ -67,8 +67,11 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
   m.b = (int)it;
   if (a.tok_start) {
     // the last row that starts at or before it; all that is needed of a row is
-    // asked for at once
+    // asked for at once. The numbers hold as long as the stretches are in order: the first row
+    // whose is not is the last that is looked at (the last item, if no other, gets
+    // there), and neither it nor a row behind has an item.
     int b = 0, r_ts = 0, r_te = 0, r_t = 0;
+    bool ordered = true;
     for (int base = 0; base < a.B; base += 32) {
       const int r = base + lane;
       int v_ts = 0, v_te = 0, v_t = 0;
@@ -77,23 +80,24 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
         v_te = __ldg(a.tok_start + r + 1);
         v_t = __ldg(a.seq_lens + r);
       }
-      const unsigned who = __ballot_sync(
-          0xffffffffu, r < a.B && (long long)v_ts / ODA_TILE + 2ll * r <= (long long)it);
+      const unsigned wrong = __ballot_sync(0xffffffffu, v_ts < 0 || v_te < v_ts || v_te > a.n_tokens);
+      const unsigned who = ((wrong & (0u - wrong)) * 2u - 1u) &    // up to the first wrong one
+          __ballot_sync(0xffffffffu, r < a.B && (long long)v_ts / ODA_TILE + 2ll * r <= (long long)it);
+      if (wrong) record_error(a.err, ODA_ERR_BOUNDS);
       if (!who) break;
       const int at = 31 - __clz(who);
       b = base + at;
       r_ts = __shfl_sync(0xffffffffu, v_ts, at);
       r_te = __shfl_sync(0xffffffffu, v_te, at);
       r_t = __shfl_sync(0xffffffffu, v_t, at);
+      ordered = !((wrong >> at) & 1u);
+      if (wrong) break;
     }
+    if (!ordered) return false;
     m.b = b;
     m.t = r_t;
     ts = r_ts;
     n = (long long)r_te - ts;
-    if (ts < 0 || n < 0 || r_te > a.n_tokens) {
-      record_error(a.err, ODA_ERR_BOUNDS);
-      return false;
-    }
     if (n == 0) return false;
     j = (int)((long long)it - (ts / ODA_TILE + 2ll * b));
   } else {

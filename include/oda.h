@@ -392,8 +392,10 @@ oda_status oda_kv8_layout(const oda_config* cfg, oda_kv8_layout_info* out);
  *   ring        ring of ALL layers in the context dtype, or NULL: receives what
  *               oda_append_kv would have written for these positions
  * Slots behind a row's last position keep what they hold. A row with n > 0 and
- * seq_lens[b] < n, a tok_start that is not ascending within [0, n_tokens], or a
- * block out of range records ODA_ERR_BOUNDS and that row or block is skipped.
+ * seq_lens[b] < n, or a block out of range, records ODA_ERR_BOUNDS and that row or
+ * block is skipped; so does a tok_start that falls or leaves [0, n_tokens], and the
+ * first row whose stretch it spoils is skipped with all rows behind it. A call
+ * with B = 0 or n_tokens = 0 does nothing.
  * No physical block may be written through two (row, column) pairs in one call:
  * its contents are then unspecified. n_tokens <= 2^31 - 1.
  */

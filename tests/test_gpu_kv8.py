@@ -938,3 +938,39 @@ def test_a_list_written_late_by_the_launch_before(torch, late_store, late, regio
         assert torch.equal(out, again) and torch.equal(lse, lse2), (step, before)
         rest = [b for b in range(5) if b not in rows]
         assert (out[rest] == 7).all()
+
+
+# ------------------------------------------------------- stretches that are not in order
+
+@pytest.mark.parametrize("starts,first", [
+    ([0, 48, 16, 64], 1),                         # rows 1 and 2 would start at the same item
+    ([0, 40, 20, 64], 1), ([0, 0, 64, 10, 64], 2), ([64, 0, 64], 0), ([0, 16, 65], 1), ([0, 65, 64], 0),
+    ([0, 20, -1, 64], 1), ([-64, 20, 64], 0), ([80, 90, 90], 0), ([0, -2 ** 31, 2 ** 31 - 1, 64], 0),
+    (list(range(0, 37)) + [35, 64, 64], 36),      # behind the first 32 rows
+    ([0] * 33 + [64, 63] + [64] * 5, 33), ([0] * 39 + [65], 38), ([0] * 64 + [-3], 63),
+])
+def test_token_starts_out_of_order(torch, starts, first):
+    """Rows before the first spoilt stretch are written and read, that one and those behind are
+    not, and the error is raised however far behind it lies."""
+    oda = pytest.importorskip("gated_local_full_b200.oda")
+    B = len(starts) - 1
+    c = Case(torch, dtype="f32", hq=1, hkv=1, d=64, rows=B, columns=5, sink=2, window=12)
+    (k, kd), (v, vd) = (c.values(1, 64, 1, 64) for _ in "kv")
+    n = [starts[b + 1] - starts[b] for b in range(first)]
+    past = [int(x) for x in c.r.integers(0, 14, B)]
+    t = [p + m for p, m in zip(past, n)] + [64] * (B - first)
+    c.ctx.append_kv8("int8", 0, 1, kd, vd, c.ints(t), c.table, c.codes, c.scales, c.ring, B,
+                     tok_start=c.ints(starts))
+    assert c.ctx.get_device_error() == oda.ERR_BOUNDS
+    if first:
+        assert starts[0] == 0
+        c.oracle_write(k, v, n, past[:first])
+    c.check()
+    out = torch.full((1, 64, 1, 64), 9.0, device="cuda")
+    c.ctx.read_kv8("int8", 0, 1, c.ints(t), c.table, c.codes, c.scales, out, None, B, tok_start=c.ints(starts))
+    assert c.ctx.get_device_error() == oda.ERR_BOUNDS
+    got = out[0, :, 0].cpu().numpy()
+    for b in range(first):
+        want = c.kv(0, b, t[b])[0][0, t[b] - n[b]:].astype(np.float32)
+        assert np.array_equal(got[starts[b]:starts[b + 1]], want), b
+    assert np.all(got[starts[first] if first else 0:] == 9)
