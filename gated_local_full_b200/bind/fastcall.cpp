@@ -33,6 +33,16 @@ long long number(PyObject* o) {
   return v;
 }
 
+// ... and one that the library takes in 32 bits.
+int whole(PyObject* o) {
+  const long long v = number(o);
+  if (v != (int)v) {
+    PyErr_SetString(PyExc_OverflowError, "an argument does not fit 32 bits");
+    throw Refused();
+  }
+  return (int)v;
+}
+
 // A tensor, or null for None.
 const at::Tensor* tensor(PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
@@ -91,7 +101,8 @@ int format(PyObject* o) {
     if (PyUnicode_CompareWithASCIIString(o, "e4m3") == 0) return ODA_KV8_E4M3;
     return 0;                            // refused by the library, as any other number
   }
-  return (int)number(o);
+  const long long v = number(o);
+  return v == (int)v ? (int)v : 0;
 }
 
 // The context: (handle, hq, hkv, head_dim, dtype).
@@ -148,19 +159,19 @@ long long tokens(const Ctx& c, const at::Tensor& x, long long layers, const char
 PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> PyObject* {
     const Ctx c = context(a[0]);
-    const long long lb = number(a[2]), le = number(a[3]);
+    const int lb = whole(a[2]), le = whole(a[3]);
     const at::Tensor* k = tensor(a[4], "k_new must be a tensor");
     const at::Tensor* v = tensor(a[5], "v_new must be a tensor");
     if (!k || !v) refuse("k_new and v_new must be tensors");
-    const long long nt = tokens(c, *k, le - lb, "k_new must have the context's dtype",
+    const long long nt = tokens(c, *k, (long long)le - lb, "k_new must have the context's dtype",
                                 "k_new must be [layers][n_tokens][hkv][d]");
     if (v->sizes() != k->sizes() || v->scalar_type() != k->scalar_type())
       refuse("k_new and v_new differ in shape or type");
     const Ptrs<8> p(a + 4);
     void* st = stream(a[13]);
     auto f = reinterpret_cast<decltype(&oda_append_kv8)>(g_fn[kAppend]);
-    return done(f(c.h, format(a[1]), (int)lb, (int)le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4),
-                  p.p[5], p.floats(6), p.p[7], (int)number(a[12]), st),
+    return done(f(c.h, format(a[1]), lb, le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4),
+                  p.p[5], p.floats(6), p.p[7], whole(a[12]), st),
                 "oda_append_kv8");
   });
 }
@@ -170,16 +181,16 @@ PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&]() -> PyObject* {
     const Ctx c = context(a[0]);
-    const long long lb = number(a[2]), le = number(a[3]);
+    const int lb = whole(a[2]), le = whole(a[3]);
     const at::Tensor* k = tensor(a[9], "k_out must be a tensor or None");
     const at::Tensor* v = tensor(a[10], "v_out must be a tensor or None");
     if (!k && !v) refuse("read_kv8 needs k_out or v_out");
     long long nt = 0;
     if (k)
-      nt = tokens(c, *k, le - lb, "k_out must have the context's dtype",
+      nt = tokens(c, *k, (long long)le - lb, "k_out must have the context's dtype",
                   "k_out must be [layers][n_tokens][hkv][d]");
     if (v) {
-      const long long m = tokens(c, *v, le - lb, "v_out must have the context's dtype",
+      const long long m = tokens(c, *v, (long long)le - lb, "v_out must have the context's dtype",
                                  "v_out must be [layers][n_tokens][hkv][d]");
       if (k && m != nt) refuse("k_out and v_out differ in length");
       nt = m;
@@ -187,8 +198,8 @@ PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<7> p(a + 4);
     void* st = stream(a[12]);
     auto f = reinterpret_cast<decltype(&oda_read_kv8)>(g_fn[kRead]);
-    return done(f(c.h, format(a[1]), (int)lb, (int)le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3],
-                  p.floats(4), p.p[5], p.p[6], (int)number(a[11]), st),
+    return done(f(c.h, format(a[1]), lb, le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3],
+                  p.floats(4), p.p[5], p.p[6], whole(a[11]), st),
                 "oda_read_kv8");
   });
 }
@@ -200,8 +211,8 @@ PyObject* full_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<9> p(a + 3);
     void* st = stream(a[14]);
     auto f = reinterpret_cast<decltype(&oda_full_attn_kv8)>(g_fn[kFull]);
-    return done(f(c.h, format(a[1]), (int)number(a[2]), p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4),
-                  p.ints(5), p.ints(6), p.p[7], p.floats(8), (int)number(a[12]), (unsigned)number(a[13]), st),
+    return done(f(c.h, format(a[1]), whole(a[2]), p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4),
+                  p.ints(5), p.ints(6), p.p[7], p.floats(8), whole(a[12]), whole(a[13]), st),
                 "oda_full_attn_kv8");
   });
 }
@@ -214,9 +225,9 @@ PyObject* range_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<11> p(a + 3);
     void* st = stream(a[16]);
     auto f = reinterpret_cast<decltype(&oda_range_attn_kv8)>(g_fn[kRange]);
-    return done(f(c.h, format(a[1]), (int)number(a[2]), p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4),
-                  p.p[5], p.floats(6), p.ints(7), p.ints(8), p.p[9], p.floats(10), (int)number(a[14]),
-                  (unsigned)number(a[15]), st),
+    return done(f(c.h, format(a[1]), whole(a[2]), p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4),
+                  p.p[5], p.floats(6), p.ints(7), p.ints(8), p.p[9], p.floats(10), whole(a[14]),
+                  whole(a[15]), st),
                 "oda_range_attn_kv8");
   });
 }
@@ -270,8 +281,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     void* st = stream(a[12]);
     auto f = reinterpret_cast<decltype(&oda_qk_norm_rope)>(g_fn[kRope]);
     return done(f(c.h, qp, qs, kp, ks, w.p[0], w.p[1], (float)eps, fp.floats(0),
-                  fr ? (int)(2 * fr->numel()) : 0, fp.ints(1), (int)number(a[10]), n, qop, qos, kop, kos,
-                  (unsigned)number(a[11]), st),
+                  fr ? (int)(2 * fr->numel()) : 0, fp.ints(1), whole(a[10]), n, qop, qos, kop, kos,
+                  whole(a[11]), st),
                 "oda_qk_norm_rope");
   });
 }

@@ -174,3 +174,45 @@ def test_write_items_never_meet():
                     assert it < items and it not in used
                     assert max(x for x in range(B) if start[x] <= it) == b
                     used.add(it)
+
+
+# ------------------------------------------------------------ the compiled calls
+
+def _bare():
+    """A binding's context without a library handle: every call ends with ODA_ERR_ARG at the latest."""
+    from gated_local_full_b200 import oda
+
+    class Ctx(oda.OdaContext):
+        def __init__(self, cfg):
+            self.cfg, self.handle = cfg, None
+
+    return Ctx(_cfg())
+
+
+def test_numbers_past_32_bits_are_refused():
+    pytest.importorskip("torch")
+    _ensure_built()
+    from gated_local_full_b200 import oda
+    ctx = _bare()
+
+    def full(layer=0, B=1, format="int8"):
+        ctx.full_attn_kv8(format, layer, 64, 64, 64, 64, 64, 64, 64, 64, None, B, stream=0)
+
+    def ranged(layer=0, B=1):
+        ctx.range_attn_kv8("int8", layer, 64, 64, 64, 64, 64, 64, 64, 64, 64, 64, None, B, stream=0)
+
+    for f in (full, ranged):
+        with pytest.raises(oda.OdaError):
+            f()
+        for v in (2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 31 - 1, 2 ** 63, 2 ** 70):
+            with pytest.raises(OverflowError):
+                f(layer=v)
+            with pytest.raises(OverflowError):
+                f(B=v)
+    torch = pytest.importorskip("torch")
+    kv = torch.zeros((1, 2, 8, 128), dtype=torch.bfloat16)
+    for v in (2 ** 32, 2 ** 33 + 1):
+        with pytest.raises(OverflowError):
+            ctx.append_kv8("int8", v, v + 1, kv, kv, 64, 64, 64, 64, None, 2, stream=0)
+        with pytest.raises(OverflowError):
+            ctx.read_kv8("int8", v, v + 1, 64, 64, 64, 64, kv, kv, 2, stream=0)
