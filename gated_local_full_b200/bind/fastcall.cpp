@@ -122,7 +122,13 @@ Ctx context(PyObject* o) {
   return c;
 }
 
-PyObject* done(int status, const char* where) {
+// Makes the call, whose arguments are all worked out, without the interpreter's lock: a launch
+// waits where the GPU's queue is full, which a host function written in Python may have to empty.
+template <typename F>
+PyObject* done(const char* where, F&& call) {
+  PyThreadState* const thread = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(thread);
   if (status == ODA_OK) Py_RETURN_NONE;
   PyObject* e = PyObject_CallFunction(g_error, "is", status, where);
   if (e) {
@@ -170,9 +176,11 @@ PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<8> p(a + 4);
     void* st = stream(a[13]);
     auto f = reinterpret_cast<decltype(&oda_append_kv8)>(g_fn[kAppend]);
-    return done(f(c.h, format(a[1]), lb, le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4),
-                  p.p[5], p.floats(6), p.p[7], whole(a[12]), st),
-                "oda_append_kv8");
+    const int fmt = format(a[1]), B = whole(a[12]);
+    return done("oda_append_kv8", [&] {
+      return f(c.h, fmt, lb, le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4), p.p[5], p.floats(6),
+               p.p[7], B, st);
+    });
   });
 }
 
@@ -198,9 +206,11 @@ PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<7> p(a + 4);
     void* st = stream(a[12]);
     auto f = reinterpret_cast<decltype(&oda_read_kv8)>(g_fn[kRead]);
-    return done(f(c.h, format(a[1]), lb, le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3],
-                  p.floats(4), p.p[5], p.p[6], whole(a[11]), st),
-                "oda_read_kv8");
+    const int fmt = format(a[1]), B = whole(a[11]);
+    return done("oda_read_kv8", [&] {
+      return f(c.h, fmt, lb, le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3], p.floats(4), p.p[5], p.p[6], B,
+               st);
+    });
   });
 }
 
@@ -211,9 +221,11 @@ PyObject* full_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<9> p(a + 3);
     void* st = stream(a[14]);
     auto f = reinterpret_cast<decltype(&oda_full_attn_kv8)>(g_fn[kFull]);
-    return done(f(c.h, format(a[1]), whole(a[2]), p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4),
-                  p.ints(5), p.ints(6), p.p[7], p.floats(8), whole(a[12]), whole(a[13]), st),
-                "oda_full_attn_kv8");
+    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[12]), flags = whole(a[13]);
+    return done("oda_full_attn_kv8", [&] {
+      return f(c.h, fmt, layer, p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4), p.ints(5), p.ints(6), p.p[7],
+               p.floats(8), B, flags, st);
+    });
   });
 }
 
@@ -225,10 +237,11 @@ PyObject* range_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ptrs<11> p(a + 3);
     void* st = stream(a[16]);
     auto f = reinterpret_cast<decltype(&oda_range_attn_kv8)>(g_fn[kRange]);
-    return done(f(c.h, format(a[1]), whole(a[2]), p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4),
-                  p.p[5], p.floats(6), p.ints(7), p.ints(8), p.p[9], p.floats(10), whole(a[14]),
-                  whole(a[15]), st),
-                "oda_range_attn_kv8");
+    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[14]), flags = whole(a[15]);
+    return done("oda_range_attn_kv8", [&] {
+      return f(c.h, fmt, layer, p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4), p.p[5], p.floats(6), p.ints(7),
+               p.ints(8), p.p[9], p.floats(10), B, flags, st);
+    });
   });
 }
 
@@ -280,10 +293,11 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (eps == -1.0 && PyErr_Occurred()) throw Refused();
     void* st = stream(a[12]);
     auto f = reinterpret_cast<decltype(&oda_qk_norm_rope)>(g_fn[kRope]);
-    return done(f(c.h, qp, qs, kp, ks, w.p[0], w.p[1], (float)eps, fp.floats(0),
-                  fr ? (int)(2 * fr->numel()) : 0, fp.ints(1), whole(a[10]), n, qop, qos, kop, kos,
-                  whole(a[11]), st),
-                "oda_qk_norm_rope");
+    const int rot = fr ? (int)(2 * fr->numel()) : 0, offset = whole(a[10]), flags = whole(a[11]);
+    return done("oda_qk_norm_rope", [&] {
+      return f(c.h, qp, qs, kp, ks, w.p[0], w.p[1], (float)eps, fp.floats(0), rot, fp.ints(1), offset, n, qop, qos,
+               kop, kos, flags, st);
+    });
   });
 }
 

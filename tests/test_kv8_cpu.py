@@ -216,3 +216,37 @@ def test_numbers_past_32_bits_are_refused():
             ctx.append_kv8("int8", v, v + 1, kv, kv, 64, 64, 64, 64, None, 2, stream=0)
         with pytest.raises(OverflowError):
             ctx.read_kv8("int8", v, v + 1, 64, 64, 64, 64, kv, kv, 2, stream=0)
+
+
+def test_calls_leave_the_interpreter_to_other_threads():
+    """With a function that sleeps in the library's place (its first argument, the context's
+    handle, is the time in us), another thread counts on while a call is under way."""
+    pytest.importorskip("torch")
+    _ensure_built()
+    import threading
+    from gated_local_full_b200 import oda
+    f = oda._fastcall()
+    sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    key = (300000,) + _bare()._context()[1:]
+    args = ("int8", 0) + (64,) * 8 + (None, 1, 0, 0)       # layer, ..., lse, B, flags, stream
+    started, seen, stop = threading.Event(), [0], threading.Event()
+
+    def count():
+        started.set()
+        while not stop.wait(0.005):
+            seen[0] += 1
+
+    other = threading.Thread(target=count)
+    try:
+        f.bind(oda.OdaError, *[sleep] * len(oda._FAST_CALLS))
+        other.start()
+        started.wait(10)
+        before = seen[0]
+        f.full_attn_kv8(key, *args)
+        after = seen[0]
+    finally:
+        stop.set()
+        other.join()
+        oda._fast = None                                   # bound to the library again by the next call
+    assert after - before >= 5
+    oda._fastcall()
