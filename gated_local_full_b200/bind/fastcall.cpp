@@ -7,6 +7,8 @@
 // binding takes from the library that it loaded.
 #include <Python.h>
 
+#include <algorithm>
+
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -72,17 +74,23 @@ void* ptr(PyObject* o) {
   return p;
 }
 
-// Several of them, in order (before the stream is asked for: it needs a GPU, and a
-// tensor that is not on one is the better thing to report).
-template <int N>
-struct Ptrs {
-  void* p[N];
-  Ptrs(PyObject* const* a) {
-    for (int i = 0; i < N; ++i) p[i] = ptr(a[i]);
+// An argument of the call. What the library is told by a pointer alone it cannot check, so a
+// tensor must have the type and at least the elements that the call reads or writes; an address
+// is the caller's word for them. (All of them before the stream is asked for: it needs a GPU, and a
+// tensor that is not on one is the better thing to report.)
+void* arg(PyObject* o, at::ScalarType type, long long least, const char* what) {
+  if (o != Py_None && !PyLong_Check(o)) {
+    const at::Tensor* x = tensor(o, "a tensor, an address or None is wanted");
+    if (x->scalar_type() != type || x->numel() < least) refuse(what);
   }
-  const int32_t* ints(int i) const { return static_cast<const int32_t*>(p[i]); }
-  float* floats(int i) const { return static_cast<float*>(p[i]); }
-};
+  return ptr(o);
+}
+const int32_t* ints(PyObject* o, long long least, const char* what) {
+  return static_cast<const int32_t*>(arg(o, at::kInt, least, what));
+}
+float* floats(PyObject* o, long long least, const char* what) {
+  return static_cast<float*>(arg(o, at::kFloat, least, what));
+}
 
 void* stream(PyObject* o) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -105,22 +113,55 @@ int format(PyObject* o) {
   return v == (int)v ? (int)v : 0;
 }
 
-// The context: (handle, hq, hkv, head_dim, dtype).
+// The context: (handle, hq, hkv, head_dim, dtype, layers, max_blocks_per_seq, num_blocks,
+// elements of a layer's ring).
 struct Ctx {
   oda_ctx* h;
   long long hq, hkv, d;
   at::ScalarType type;
+  long long layers, max_blocks, num_blocks, ring;
 };
 Ctx context(PyObject* o) {
-  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) refuse("not a context");
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 9) refuse("not a context");
+  const auto item = [&](int i) { return number(PyTuple_GET_ITEM(o, i)); };
   Ctx c;
   c.h = static_cast<oda_ctx*>(ptr(PyTuple_GET_ITEM(o, 0)));
-  c.hq = number(PyTuple_GET_ITEM(o, 1));
-  c.hkv = number(PyTuple_GET_ITEM(o, 2));
-  c.d = number(PyTuple_GET_ITEM(o, 3));
-  c.type = number(PyTuple_GET_ITEM(o, 4)) == ODA_BF16 ? at::kBFloat16 : at::kFloat;
+  c.hq = item(1);
+  c.hkv = item(2);
+  c.d = item(3);
+  c.type = item(4) == ODA_BF16 ? at::kBFloat16 : at::kFloat;
+  c.layers = item(5);
+  c.max_blocks = item(6);
+  c.num_blocks = item(7);
+  c.ring = item(8);
   return c;
 }
+
+// The row lists and the cache that the calls share. `layers`: how many the call reaches, from
+// layer 0 on (one that the context does not have is the library's to refuse).
+struct Cache {
+  const int32_t *seq_lens, *table;
+  void* codes;
+  float* scales;
+  Cache(const Ctx& c, long long layers, long long B, PyObject* lens, PyObject* tab, PyObject* co, PyObject* sc) {
+    seq_lens = ints(lens, B, "seq_lens must be int32 [B]");
+    const char* const columns = "block_table must be int32 [B][max_blocks_per_seq]";
+    if (THPVariable_Check(tab)) {
+      const at::Tensor& x = THPVariable_Unpack(tab);
+      if (x.dim() == 2 && x.size(1) != c.max_blocks) refuse(columns);
+    }
+    table = ints(tab, B * c.max_blocks, columns);
+    const long long halves = std::min(layers, c.layers) * c.num_blocks * c.hkv * 2;
+    if (THPVariable_Check(co)) {
+      const at::Tensor& x = THPVariable_Unpack(co);
+      if (x.element_size() != 1 || x.numel() < halves * 16 * c.d)
+        refuse("codes must be of one byte, [layers][num_blocks][hkv][2][16][d]");
+    }
+    codes = ptr(co);
+    scales = floats(sc, halves, "scales must be float32 [layers][num_blocks][hkv][2]");
+  }
+};
+const char* const kStarts = "tok_start must be int32 [B + 1]";
 
 // Makes the call, whose arguments are all worked out, without the interpreter's lock: a launch
 // waits where the GPU's queue is full, which a host function written in Python may have to empty.
@@ -173,13 +214,15 @@ PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 "k_new must be [layers][n_tokens][hkv][d]");
     if (v->sizes() != k->sizes() || v->scalar_type() != k->scalar_type())
       refuse("k_new and v_new differ in shape or type");
-    const Ptrs<8> p(a + 4);
-    void* st = stream(a[13]);
-    auto f = reinterpret_cast<decltype(&oda_append_kv8)>(g_fn[kAppend]);
     const int fmt = format(a[1]), B = whole(a[12]);
+    const int32_t* starts = ints(a[6], B + 1ll, kStarts);
+    const Cache h(c, le, B, a[7], a[8], a[9], a[10]);
+    void* ring = arg(a[11], c.type, std::min<long long>(le, c.layers) * c.ring,
+                     "ring must have the context's dtype and layout");
+    void *kp = ptr(a[4]), *vp = ptr(a[5]), *st = stream(a[13]);
+    auto f = reinterpret_cast<decltype(&oda_append_kv8)>(g_fn[kAppend]);
     return done("oda_append_kv8", [&] {
-      return f(c.h, fmt, lb, le, p.p[0], p.p[1], p.ints(2), nt, p.ints(3), p.ints(4), p.p[5], p.floats(6),
-               p.p[7], B, st);
+      return f(c.h, fmt, lb, le, kp, vp, starts, nt, h.seq_lens, h.table, h.codes, h.scales, ring, B, st);
     });
   });
 }
@@ -203,28 +246,43 @@ PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (k && m != nt) refuse("k_out and v_out differ in length");
       nt = m;
     }
-    const Ptrs<7> p(a + 4);
-    void* st = stream(a[12]);
-    auto f = reinterpret_cast<decltype(&oda_read_kv8)>(g_fn[kRead]);
     const int fmt = format(a[1]), B = whole(a[11]);
+    const int32_t* starts = ints(a[4], B + 1ll, kStarts);
+    const Cache h(c, le, B, a[5], a[6], a[7], a[8]);
+    void *kp = ptr(a[9]), *vp = ptr(a[10]), *st = stream(a[12]);
+    auto f = reinterpret_cast<decltype(&oda_read_kv8)>(g_fn[kRead]);
     return done("oda_read_kv8", [&] {
-      return f(c.h, fmt, lb, le, p.ints(0), nt, p.ints(1), p.ints(2), p.p[3], p.floats(4), p.p[5], p.p[6], B,
-               st);
+      return f(c.h, fmt, lb, le, starts, nt, h.seq_lens, h.table, h.codes, h.scales, kp, vp, B, st);
     });
   });
 }
+
+// What both attention calls take beside the cache and the regions.
+struct Rows {
+  void *q, *out;
+  const int32_t *idx, *count;
+  float* lse;
+  Rows(const Ctx& c, long long B, PyObject* q_, PyObject* idx_, PyObject* count_, PyObject* out_, PyObject* lse_) {
+    q = arg(q_, c.type, B * c.hq * c.d, "q must be [B][hq][d] of the context's dtype");
+    idx = ints(idx_, B, "idx must be int32 [B]");
+    count = ints(count_, 1, "count must be int32 [1]");
+    out = arg(out_, c.type, B * c.hq * c.d, "out must be [B][hq][d] of the context's dtype");
+    lse = floats(lse_, B * c.hq, "lse must be float32 [B][hq]");
+  }
+};
 
 // ctx, format, layer, q, seq_lens, block_table, codes, scales, idx, count, out, lse, B, flags, stream
 PyObject* full_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject* {
     const Ctx c = context(a[0]);
-    const Ptrs<9> p(a + 3);
+    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[12]), flags = whole(a[13]);
+    const Rows r(c, B, a[3], a[8], a[9], a[10], a[11]);
+    const Cache h(c, layer + 1ll, B, a[4], a[5], a[6], a[7]);
     void* st = stream(a[14]);
     auto f = reinterpret_cast<decltype(&oda_full_attn_kv8)>(g_fn[kFull]);
-    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[12]), flags = whole(a[13]);
     return done("oda_full_attn_kv8", [&] {
-      return f(c.h, fmt, layer, p.p[0], p.ints(1), p.ints(2), p.p[3], p.floats(4), p.ints(5), p.ints(6), p.p[7],
-               p.floats(8), B, flags, st);
+      return f(c.h, fmt, layer, r.q, h.seq_lens, h.table, h.codes, h.scales, r.idx, r.count, r.out, r.lse, B, flags,
+               st);
     });
   });
 }
@@ -234,13 +292,16 @@ PyObject* full_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* range_attn_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 17, [&]() -> PyObject* {
     const Ctx c = context(a[0]);
-    const Ptrs<11> p(a + 3);
+    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[14]), flags = whole(a[15]);
+    const Rows r(c, B, a[3], a[10], a[11], a[12], a[13]);
+    const int32_t* lo = ints(a[5], B, "range_lo must be int32 [B]");
+    const int32_t* hi = ints(a[6], B, "range_hi must be int32 [B]");
+    const Cache h(c, layer + 1ll, B, a[4], a[7], a[8], a[9]);
     void* st = stream(a[16]);
     auto f = reinterpret_cast<decltype(&oda_range_attn_kv8)>(g_fn[kRange]);
-    const int fmt = format(a[1]), layer = whole(a[2]), B = whole(a[14]), flags = whole(a[15]);
     return done("oda_range_attn_kv8", [&] {
-      return f(c.h, fmt, layer, p.p[0], p.ints(1), p.ints(2), p.ints(3), p.ints(4), p.p[5], p.floats(6), p.ints(7),
-               p.ints(8), p.p[9], p.floats(10), B, flags, st);
+      return f(c.h, fmt, layer, r.q, h.seq_lens, lo, hi, h.table, h.codes, h.scales, r.idx, r.count, r.out, r.lse, B,
+               flags, st);
     });
   });
 }
@@ -288,15 +349,17 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     void* qop = heads(c, *qo, qos);
     void* kp = k ? heads(c, *k, ks) : nullptr;
     void* kop = ko ? heads(c, *ko, kos) : nullptr;
-    const Ptrs<2> w(a + 3), fp(a + 6);
+    void *qw = ptr(a[3]), *kw = ptr(a[4]);
+    const float* freq = static_cast<const float*>(ptr(a[6]));
+    const int32_t* at_pos = static_cast<const int32_t*>(ptr(a[7]));
     const double eps = PyFloat_AsDouble(a[5]);
     if (eps == -1.0 && PyErr_Occurred()) throw Refused();
     void* st = stream(a[12]);
     auto f = reinterpret_cast<decltype(&oda_qk_norm_rope)>(g_fn[kRope]);
     const int rot = fr ? (int)(2 * fr->numel()) : 0, offset = whole(a[10]), flags = whole(a[11]);
     return done("oda_qk_norm_rope", [&] {
-      return f(c.h, qp, qs, kp, ks, w.p[0], w.p[1], (float)eps, fp.floats(0), rot, fp.ints(1), offset, n, qop, qos,
-               kop, kos, flags, st);
+      return f(c.h, qp, qs, kp, ks, qw, kw, (float)eps, freq, rot, at_pos, offset, n, qop, qos, kop, kos, flags,
+               st);
     });
   });
 }

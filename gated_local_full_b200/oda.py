@@ -288,10 +288,11 @@ class OdaContext:
     _key = None
 
     def _context(self):
-        """(handle, hq, hkv, head_dim, dtype) for the compiled calls."""
+        """What the compiled calls know of the context (bind/fastcall.cpp, Ctx)."""
         if self._key is None:
             c = self.cfg
-            self._key = (self.handle.value if self.handle else None, c.hq, c.hkv, c.head_dim, c.dtype)
+            self._key = (self.handle.value if self.handle else None, c.hq, c.hkv, c.head_dim, c.dtype,
+                         c.layers, c.max_blocks_per_seq, c.num_blocks, layout(c)["ring_layer_elems"])
         return self._key
 
     # ------------------------------------------------------------- the path
@@ -367,7 +368,9 @@ class OdaContext:
                "oda_range_attn")
 
     # ------------------------------------------------------ the 8-bit cache
-    # format: "int8" or "e4m3" (or KV8_INT8, KV8_E4M3)
+    # format: "int8" or "e4m3" (or KV8_INT8, KV8_E4M3). A tensor of another type than the header
+    # states, or with fewer elements than the call reads or writes, is a ValueError; so is one that is
+    # not contiguous (qk_norm_rope alone takes views) or not on the current GPU.
     def append_kv8(self, format, layer_begin, layer_end, k_new, v_new, seq_lens, block_table,
                    codes, scales, ring, B, tok_start=None, stream=None):
         """Quantise the rows' new tokens into the 8-bit cache, and into the ring as

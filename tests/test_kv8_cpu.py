@@ -250,3 +250,85 @@ def test_calls_leave_the_interpreter_to_other_threads():
         oda._fast = None                                   # bound to the library again by the next call
     assert after - before >= 5
     oda._fastcall()
+
+
+@pytest.mark.parametrize("region", [False, True], ids=["full", "region"])
+def test_types_and_sizes_of_the_attention_calls(region):
+    """A tensor in a wrong type, or shorter than what the call would read or write, is refused for that
+    (before its place is looked at); a right one only for not being on a GPU."""
+    torch = pytest.importorskip("torch")
+    _ensure_built()
+    from gated_local_full_b200 import oda
+    ctx = _bare()
+    ctx.cfg = _cfg(layers=2, max_blocks_per_seq=5, num_blocks=7)
+    i32, f32, b16, u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+    right = dict(q=((3, 16, 128), b16), seq_lens=((3,), i32), block_table=((3, 5), i32),
+                 codes=((2, 7, 8, 2, 16, 128), u8), scales=((2, 7, 8, 2), f32), idx=((3,), i32), count=((1,), i32),
+                 out=((3, 16, 128), b16), lse=((3, 16), f32))
+    if region:
+        right.update(range_lo=((3,), i32), range_hi=((3,), i32))
+    f = ctx.range_attn_kv8 if region else ctx.full_attn_kv8
+    names = [n for n in ("q", "seq_lens", "range_lo", "range_hi", "block_table", "codes", "scales", "idx", "count", "out",
+                         "lse") if n in right]
+
+    def call(name, x, layer=1, B=3):
+        f("int8", layer, *[x if n == name else 64 for n in names], B, stream=0)
+
+    for name in names:
+        shape, kind = right[name]
+        with pytest.raises(ValueError, match="GPU"):
+            call(name, torch.zeros(shape, dtype=kind))
+        with pytest.raises(ValueError, match="GPU"):
+            call(name, torch.zeros(int(np.prod(shape)) + 1, dtype=kind))
+        for other in {torch.int64, f32, b16, torch.float16, i32, u8} - {kind}:
+            with pytest.raises(ValueError, match=name):
+                call(name, torch.zeros(shape, dtype=other))
+        with pytest.raises(ValueError, match=name):
+            call(name, torch.zeros(int(np.prod(shape)) - 1, dtype=kind))
+        if name in ("codes", "scales"):                    # what layer 0 alone needs
+            with pytest.raises(ValueError, match="GPU"):
+                call(name, torch.zeros(shape[1:], dtype=kind), layer=0)
+        elif name != "count":
+            with pytest.raises(ValueError, match=name):
+                call(name, torch.zeros(shape, dtype=kind), B=4)
+    for wide in (4, 6, 15):                                # rows of another length
+        with pytest.raises(ValueError, match="block_table"):
+            call("block_table", torch.zeros((30, wide), dtype=i32))
+    for e in (torch.int8, torch.float8_e4m3fn):            # codes seen as what they hold
+        with pytest.raises(ValueError, match="GPU"):
+            call("codes", torch.zeros((2, 7, 8, 2, 16, 128), dtype=torch.int8).view(e))
+    with pytest.raises(oda.OdaError):                      # a layer that there is none of: the library's answer
+        call("q", 64, layer=2 ** 31 - 1)
+
+
+def test_types_and_sizes_of_the_lists_of_write_and_read():
+    torch = pytest.importorskip("torch")
+    _ensure_built()
+    ctx = _bare()
+    ctx.cfg = _cfg(layers=2, max_blocks_per_seq=5, num_blocks=7, window=12, max_batch=3)
+    kv = torch.zeros((1, 9, 8, 128), dtype=torch.bfloat16)
+    right = dict(tok_start=((4,), torch.int32), seq_lens=((3,), torch.int32), block_table=((3, 5), torch.int32),
+                 codes=((2, 7, 8, 2, 16, 128), torch.uint8), scales=((2, 7, 8, 2), torch.float32),
+                 ring=((2, 3, 8, 1, 2, 16, 128), torch.bfloat16))
+
+    def append(name, x):
+        a = {n: x if n == name else 64 for n in right}
+        ctx.append_kv8("e4m3", 1, 2, kv, kv, a["seq_lens"], a["block_table"], a["codes"], a["scales"], a["ring"], 3,
+                       tok_start=a["tok_start"], stream=0)
+
+    def read(name, x):
+        a = {n: x if n == name else 64 for n in right}
+        ctx.read_kv8("e4m3", 1, 2, a["seq_lens"], a["block_table"], a["codes"], a["scales"], kv, None, 3,
+                     tok_start=a["tok_start"], stream=0)
+
+    for f in (append, read):
+        for name, (shape, kind) in right.items():
+            if f is read and name == "ring":
+                continue
+            with pytest.raises(ValueError, match="GPU"):
+                f(name, torch.zeros(shape, dtype=kind))
+            for other in {torch.int64, torch.float64} - {kind}:
+                with pytest.raises(ValueError, match=name):
+                    f(name, torch.zeros(shape, dtype=other))
+            with pytest.raises(ValueError, match=name):
+                f(name, torch.zeros(int(np.prod(shape)) - 1, dtype=kind))
