@@ -11,18 +11,20 @@
 // the tokens as the products' 16 rows (scores) or depth (values):
 //   * Scores, e4m3: the codes become f16, exactly, and mma.sync m16n8k16 sums in
 //     float32. A power of two per head puts the query's largest element into
-//     [1, 2); it is then one f16 number (bfloat16: exact down to 2^-17 of the
-//     largest, and within 2^-25 of it below), or two (float32: the second is 2^11
-//     times what is left), in columns of their own.
+//     [1, 2); an element is then one f16 number and a second, 2^11 times what is left, in
+//     columns of their own: within 2^-22 of itself, or 2^-36 of the largest (bfloat16: exact
+//     down to 2^-28 of the largest).
 //   * Scores, int8: the codes go into mma.sync m16n8k32 as they are, so the query
 //     is written in whole numbers: a power of two per head makes its largest
 //     element 2^29 .. 2^30, and four balanced digits to the base 256 are four
 //     columns. The sums are exact; 2^-30 of the largest element is lost.
-//     (e4m3 products of that instruction are converted to f16 by the compiler,
-//     query and all, for each: 20 cycles against 16 for the two f16 products.)
+//     (For e4m3 that instruction's e4m3 form measured 20 cycles, the two f16 products 16.)
 //   * The softmax weight times the value's scale, w_j = 2^(s_j - m) R with R =
-//     vscale 2^(m - M + 11), is split into an f16 part and the f16 rest, 22 bits
-//     in all, in two columns; the codes of V become f16. M is a reference for
+//     vscale 2^(m - M + 11), is split into an f16 part and 2^11 times the rest, in two
+//     columns with accumulators of their own; the codes of V become f16. So w_j is within
+//     2^-22 of itself or, more than 2^25 below the reference, 2^-47 of that: a block far above the
+//     others in one dim leaves the others' shares of the rest. (With the rest unscaled it was 2^-36,
+//     and a block 2^40 above lost all else.) M is a reference for
 //     s_j + log2 vscale (what the value accumulators are relative to), kept apart
 //     from the reference m of s_j (what the sum l is relative to): a block with
 //     a tiny scale then cannot push another block's weights out of f16. Both are
@@ -201,7 +203,7 @@ struct State {
   uint32_t qf[FMT == kInt8 ? 2 * KC * SETS : 4 * KC][2];
   float qs;                              // this lane's head: what its sums count for, times the scores' scale
   float m, M, l, K;                      // K = 2^(m - M + kLift), infinite while M is kNone
-  float acc[Tile<D>::MT][4];             // [0] + [1]: one dim of this lane's head, [2] + [3]: the next
+  float acc[Tile<D>::MT][4];             // [0] + [1] 2^-11: one dim of this lane's head, [2] + [3] 2^-11: the next
 
   __device__ __forceinline__ void reset() {
     m = M = kNone;
@@ -348,7 +350,7 @@ struct State {
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        s[i] = sizeof(T) == 4 ? fmaf(c[2 * i + 1], 0x1p-11f, c[2 * i]) : c[2 * i];
+        s[i] = fmaf(c[2 * i + 1], 0x1p-11f, c[2 * i]);
     }
   }
 
@@ -413,12 +415,12 @@ struct State {
         }
     }
     l += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
-    // row g: this lane's two columns are the weight's f16 part and its rest
+    // row g: this lane's two columns are the weight's f16 part and 2^11 times its rest
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        b[t][i] = transpose8x8(pack_f16(w[t][i], w[t][i] - __half2float(__float2half_rn(w[t][i]))));
+        b[t][i] = transpose8x8(pack_f16(w[t][i], (w[t][i] - __half2float(__float2half_rn(w[t][i]))) * 0x1p11f));
   }
 
   __device__ __forceinline__ void values(const uint32_t (&v)[4][Tile<D>::VW], const uint32_t (&b)[2]) {
@@ -450,8 +452,8 @@ struct State {
     float* w = ws + h * (D + 4);
 #pragma unroll
     for (int i = 0; i < Tile<D>::MT; ++i) {
-      w[g * (D / 8) + 2 * i] = acc[i][0] + acc[i][1];
-      w[g * (D / 8) + 2 * i + 1] = acc[i][2] + acc[i][3];
+      w[g * (D / 8) + 2 * i] = fmaf(acc[i][1], 0x1p-11f, acc[i][0]);
+      w[g * (D / 8) + 2 * i + 1] = fmaf(acc[i][3], 0x1p-11f, acc[i][2]);
     }
     if (g == 0) {
       w[D] = M;

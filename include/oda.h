@@ -419,9 +419,12 @@ oda_status oda_read_kv8(oda_ctx* ctx, int format, int layer_begin, int layer_end
 /*
  * oda_full_attn_gated and oda_range_attn over the 8-bit cache: the same rows,
  * regions, layouts, outputs and errors, K and V being code * scale. The scales
- * are applied to scores and weights in float32; queries and weights go through
- * the tensor cores with at least 22 bits, so the result is that of float32
- * arithmetic on the stored values. flags: 0 or ODA_ATTN_INPUTS_READY, which then
+ * are applied to scores and weights in float32, and every sum is float32. What goes
+ * through the tensor cores is held to 2^-22 of itself or, if that is more: a query
+ * element to 2^-36 (ODA_KV8_INT8: 2^-30) of its head's largest, and a weight p_j times
+ * its block's scale of V to 2^-47 of the largest such product of the row. A result
+ * so differs from float32 arithmetic on the stored values only where an element rests
+ * on numbers that far below others. flags: 0 or ODA_ATTN_INPUTS_READY, which then
  * covers codes and scales. Slots of a block outside the row's positions or the
  * region may hold anything.
  */

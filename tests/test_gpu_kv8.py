@@ -974,3 +974,92 @@ def test_token_starts_out_of_order(torch, starts, first):
         want = c.kv(0, b, t[b])[0][0, t[b] - n[b]:].astype(np.float32)
         assert np.array_equal(got[starts[b]:starts[b + 1]], want), b
     assert np.all(got[starts[first] if first else 0:] == 9)
+
+
+# ------------------------------------------------------------ what is held in fewer bits
+
+def held_bound(q, K, V, fmt, dtype, scales):
+    """attn_bound, and what the forms of queries and weights lose below their range: a query element is
+    held to 2^-22 of itself (counted there) or to 2^-36 (int8: 2^-30) of its head's largest, which
+    moves a score by D = 2^-36 max|q| sum|k| / sqrt(d) and weights by a factor within exp(2 D); a weight
+    times its block's scale to 2^-22 of itself (counted there) or to 2^-47 of the row's largest."""
+    d, n = q.shape[1], K.shape[1]
+    group = q.shape[0] // K.shape[0]
+    more = []
+    for h in range(q.shape[0]):
+        k, v = K[h // group], V[h // group]
+        s = k @ q[h] / np.sqrt(d)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        D = (2.0 ** -30 if fmt == "int8" else 2.0 ** -36) * np.abs(q[h]).max() * np.abs(k).sum(1).max() / np.sqrt(d)
+        if dtype == "bf16" and np.abs(q[h]).max() <= 2.0 ** 22 * np.abs(q[h])[q[h] != 0].min():
+            D = 0.0                                          # bf16 has 8 bits: held whole
+        scale = scales[h // group].repeat(16)[:n]
+        codes = np.abs(v) / np.where(scale > 0, scale, 1.0)[:, None]
+        more.append(2 * np.expm1(2 * D) * (p @ np.abs(v)) + 2.0 ** -47 * (p * scale).max() * codes.sum(0))
+    return attn_bound(q, K, V, 1, n + 1, dtype) + np.array(more)
+
+
+def v_scales(c, b, t):
+    return c.scales_h[0, c.table_h[b, :(t + 15) // 16], :, 1].astype(np.float64).T
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_block_with_one_large_dim(torch, fmt, dtype):
+    """A block whose V is far above the others' in one dim and zero in the rest, early, late and in the
+    middle of the rows: the other dims are those of the other blocks' tokens."""
+    up = [0, 12, 24, 40]
+    t = [700, 650, 300, 200]
+    c = Case(torch, fmt=fmt, dtype=dtype, hq=2, hkv=1, d=64, rows=4, columns=44)
+    (k, kd), (v, _) = (c.values(1, sum(t), 1, 64) for _ in "kv")
+    at = c.starts(t)
+    for b, e in enumerate(up):
+        for block in (1, 3, (t[b] // 16) // 2, t[b] // 16 - 1):
+            s = slice(at[b] + 16 * block, at[b] + 16 * block + 16)
+            v[:, s, :, 1:] = 0.0
+            v[:, s, :, 0] = (2.0 ** e) * (1 + (v[:, s, :, 0] > 0))
+    c.ctx.append_kv8(fmt, 0, 1, kd, torch.from_numpy(v).to(c.kind).cuda(), c.ints(t), c.table, c.codes, c.scales,
+                     None, 4, tok_start=c.ints(at))
+    c.oracle_write(k, v, t, [0] * 4, ring=False)
+    c.check()
+    q, qd = c.values(4, 2, 64)
+    out, lse = torch.zeros((4, 2, 64), dtype=c.kind, device="cuda"), torch.zeros((4, 2), device="cuda")
+    idx, count = listed(c, range(4), 4)
+    c.ctx.full_attn_kv8(fmt, 0, qd, c.ints(t), c.table, c.codes, c.scales, idx, count, out, lse, 4)
+    assert c.ctx.get_device_error() == 0
+    got = out.double().cpu().numpy()
+    for b in range(4):
+        K, V = c.kv(0, b, t[b])
+        want, _ = O.full_attention(q[b], K, V, t[b])
+        err, bound = np.abs(got[b] - want), held_bound(q[b], K, V, fmt, dtype, v_scales(c, b, t[b]))
+        assert np.all(err <= bound), (b, (err / bound).max())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_query_with_one_large_element(torch, fmt, dtype):
+    """A query element 2^12 to 2^26 above the others, where the keys are zero: the scores are the others'."""
+    up = [12, 18, 21, 26]
+    t = [90, 200, 33, 400]
+    c = Case(torch, fmt=fmt, dtype=dtype, hq=2, hkv=1, d=64, rows=4, columns=25)
+    (k, _), (v, vd) = (c.values(1, sum(t), 1, 64) for _ in "kv")
+    k[..., 7] = 0.0
+    c.ctx.append_kv8(fmt, 0, 1, torch.from_numpy(k).to(c.kind).cuda(), vd, c.ints(t), c.table, c.codes, c.scales,
+                     None, 4, tok_start=c.ints(c.starts(t)))
+    c.oracle_write(k, v, t, [0] * 4, ring=False)
+    q, _ = c.values(4, 2, 64)
+    q = np.where(np.abs(q) < 0.5, np.where(q < 0, -0.5, 0.5), q)   # no element far below the others
+    for b, e in enumerate(up):
+        q[b, :, 7] = 2.0 ** e
+    qd = torch.from_numpy(q).to(c.kind).cuda()
+    out, lse = torch.zeros((4, 2, 64), dtype=c.kind, device="cuda"), torch.zeros((4, 2), device="cuda")
+    idx, count = listed(c, range(4), 4)
+    c.ctx.full_attn_kv8(fmt, 0, qd, c.ints(t), c.table, c.codes, c.scales, idx, count, out, lse, 4)
+    assert c.ctx.get_device_error() == 0
+    got = out.double().cpu().numpy()
+    for b in range(4):
+        K, V = c.kv(0, b, t[b])
+        want, _ = O.full_attention(q[b], K, V, t[b])
+        err, bound = np.abs(got[b] - want), held_bound(q[b], K, V, fmt, dtype, v_scales(c, b, t[b]))
+        assert np.all(err <= bound), (b, (err / bound).max())
