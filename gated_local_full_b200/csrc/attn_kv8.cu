@@ -689,11 +689,13 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
   __shared__ int sinfo[10];
   __shared__ Walk swalk;
   __shared__ int slast;
-  __shared__ int waited;
+  __shared__ int waited;                                     // the dependency wait is over
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_addr(smem + lay.full) + 8 * warp * ns;
   if (lane < ns) mbar_init(full + 8 * lane, 4);              // the codes' bytes and the scales of two tiles
   fence_mbar_init();
+  if (tid == 0) waited = 0;
+  __syncthreads();
   if (warp == 0) {
     // Before the dependency wait: the partition from lists that the launch before may
     // still be writing (every value is checked before it is used as an index), and
@@ -724,7 +726,6 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
       __syncwarp();
     }
   } else if (!a.early) {
-    if (tid == 32) *const_cast<volatile int*>(&waited) = 0;
     pdl_wait();
     pdl_launch_dependents();
     if (tid == 32) *const_cast<volatile int*>(&waited) = 1;
