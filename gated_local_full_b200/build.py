@@ -1,9 +1,11 @@
 """Build liboda.so (and the synthetic-input fill library) in-tree for sm_100a, and
 the binding's compiled calls.
 
-    python -m gated_local_full_b200.build [--verbose]
+    python -m gated_local_full_b200.build [--verbose] [--library]
 
-Each .cu file is compiled to an object in parallel, then linked into a shared
+The libraries need nvcc; the binding's calls also a g++ with C++20 and the headers of
+the torch that they are used with. --library leaves them out, for a program that
+uses the C ABI alone. Each .cu file is compiled to an object in parallel, then linked into a shared
 library beside this file. Nothing is JIT-compiled at import time.
 """
 
@@ -84,20 +86,21 @@ def _build_fastcall() -> str:
     return lib
 
 
-def build(verbose: bool = False) -> list:
-    """Compile liboda.so, libsynth.so and the binding's calls; returns their paths."""
+def build(verbose: bool = False, binding: bool = True) -> list:
+    """Compile liboda.so, libsynth.so and (binding) the binding's calls; returns their paths."""
     inc = ["-I", os.path.join(ROOT, "include")]
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        bind = ex.submit(_build_fastcall)
+        bind = ex.submit(_build_fastcall) if binding else None
         oda = _build_lib("liboda.so", os.path.join(PKG, "csrc"), PKG, verbose, inc)
         syn_dir = os.path.join(ROOT, "synth")
         syn = _build_lib("libsynth.so", os.path.join(syn_dir, "csrc"), syn_dir, verbose)
-        return [oda, syn, bind.result()]
+        return [oda, syn] + ([bind.result()] if bind else [])
 
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--verbose", action="store_true")
+    ap.add_argument("--library", action="store_true", help="the C ABI alone, without the binding's calls")
     a = ap.parse_args()
-    for p in build(a.verbose):
+    for p in build(a.verbose, binding=not a.library):
         print(p)

@@ -332,3 +332,17 @@ def test_types_and_sizes_of_the_lists_of_write_and_read():
                     f(name, torch.zeros(shape, dtype=other))
             with pytest.raises(ValueError, match=name):
                 f(name, torch.zeros(int(np.prod(shape)) - 1, dtype=kind))
+
+
+def test_the_library_builds_without_the_binding(monkeypatch):
+    """The C ABI's users need neither torch's headers nor g++: only the binding does."""
+    from gated_local_full_b200 import build as b
+
+    def absent():
+        raise RuntimeError("no headers")
+
+    monkeypatch.setattr(b, "_build_fastcall", absent)
+    monkeypatch.setattr(b, "_build_lib", lambda name, *a: name)
+    assert b.build(binding=False) == ["liboda.so", "libsynth.so"]
+    with pytest.raises(RuntimeError, match="no headers"):
+        b.build()
