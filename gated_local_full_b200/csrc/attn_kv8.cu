@@ -189,6 +189,7 @@ struct Tile {
 };
 
 constexpr float kLift = 11.f;            // weights are at most 2^15 < 65504
+constexpr float kUnlift = 0x1p-11f;
 
 // The head of a lane's scores: of up to two a segment, or (wide) of up to four.
 __device__ __forceinline__ int head_of(int tg, bool wide) { return (tg >> 1) + (wide ? 2 * (tg & 1) : 0); }
@@ -202,7 +203,7 @@ struct State {
   // heads; e4m3: of one word)
   uint32_t qf[FMT == kInt8 ? 2 * KC * SETS : 4 * KC][2];
   float qs;                              // this lane's head: what its sums count for, times the scores' scale
-  float m, M, l, K;                      // K = 2^(m - M + kLift), infinite while M is kNone
+  float m, M, l, K;                      // K = 2^(m - M + kLift), infinite past float32 or while M is kNone
   float acc[Tile<D>::MT][4];             // [0] + [1] 2^-11: one dim of this lane's head, [2] + [3] 2^-11: the next
 
   __device__ __forceinline__ void reset() {
@@ -405,7 +406,8 @@ struct State {
       l *= fast_exp2(m - m_new);
       m = m_new;
       M = M_new;
-      K = M == kNone ? INFINITY : fast_exp2(fminf(fmaxf(m - M + kLift, -126.f), 126.f));
+      // (infinite where it leaves float32, since only blocks of zeros reach m: the exact way each time)
+      K = M == kNone || m - M + kLift > 126.f ? INFINITY : fast_exp2(fmaxf(m - M + kLift, -126.f));
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -441,7 +443,7 @@ struct State {
     }
   }
 
-  // This warp's (acc, M, m, l) for every head: ws [G][D + 4].
+  // This warp's (acc 2^-kLift, M, m, l) for every head: ws [G][D + 4].
   __device__ __forceinline__ void store(float* ws, int G, int lane) {
     const int g = lane >> 2, tg = lane & 3;
     l += __shfl_xor_sync(0xffffffffu, l, 4);
@@ -452,8 +454,8 @@ struct State {
     float* w = ws + h * (D + 4);
 #pragma unroll
     for (int i = 0; i < Tile<D>::MT; ++i) {
-      w[g * (D / 8) + 2 * i] = fmaf(acc[i][1], 0x1p-11f, acc[i][0]);
-      w[g * (D / 8) + 2 * i + 1] = fmaf(acc[i][3], 0x1p-11f, acc[i][2]);
+      w[g * (D / 8) + 2 * i] = fmaf(acc[i][1], kUnlift * 0x1p-11f, acc[i][0] * kUnlift);
+      w[g * (D / 8) + 2 * i + 1] = fmaf(acc[i][3], kUnlift * 0x1p-11f, acc[i][2] * kUnlift);
     }
     if (g == 0) {
       w[D] = M;
@@ -891,8 +893,10 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         const float4 x = *reinterpret_cast<const float4*>(ws + w * G * (D + 4) + dd);
         if (tail[w].z == 0.f) continue;                      // no token (a NaN is not left out)
         lt += tail[w].z * fast_exp2(tail[w].y - mt);
-        const float f = fast_exp2(tail[w].x - kLift - mt);   // M = kNone: 0, or the NaN of a NaN scale
-        at4.x += x.x * f; at4.y += x.y * f; at4.z += x.z * f; at4.w += x.w * f;
+        // M = kNone: 0, or the NaN of a NaN scale. (M may lie further below mt than float32 reaches: in
+        // two halves what counts is the product.)
+        const float f = fast_exp2(0.5f * (tail[w].x - mt));
+        at4.x += x.x * f * f; at4.y += x.y * f * f; at4.z += x.z * f * f; at4.w += x.w * f * f;
       }
       if (nparts == 1) {
         const float inv = lt != 0.f ? 1.f / lt : 0.f;

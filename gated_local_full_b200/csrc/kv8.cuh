@@ -2,8 +2,9 @@
 //
 // A block's codes of one KV head and of K or V share one float32 scale:
 //   scale = max |x| / top, kept at least as large as before while the block
-//           fills (0 below 2^-107, where 1 / scale would leave float32;
-//           NaN when a value is not finite);
+//           fills (0 below 2^-107, well before 1 / scale and what the
+//           attention makes of a scale leave float32; NaN when a value is not
+//           finite);
 //   code  = round_to_format(x * (1 / scale)), value = code * scale.
 // scale, 1 / scale and the products are single float32 roundings, so a host or
 // another kernel that follows the formula gets the same codes. The one step

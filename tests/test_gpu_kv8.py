@@ -1063,3 +1063,39 @@ def test_a_query_with_one_large_element(torch, fmt, dtype):
         want, _ = O.full_attention(q[b], K, V, t[b])
         err, bound = np.abs(got[b] - want), held_bound(q[b], K, V, fmt, dtype, v_scales(c, b, t[b]))
         assert np.all(err <= bound), (b, (err / bound).max())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("apart", [10, 30, 60, 90])
+def test_small_values_far_below_the_largest_weight(torch, fmt, apart):
+    """Tokens whose V is zero have the largest weights by 2^20; the others' V is 2^-(6 + apart) and less:
+    the output is theirs alone, however small (no smaller than float32's normal numbers)."""
+    t = 30 * 16
+    c = Case(torch, fmt=fmt, dtype="f32", hq=2, hkv=1, d=64, rows=1, columns=30)
+    (k, _), (v, _) = (c.values(1, t, 1, 64) for _ in "kv")
+    high = np.zeros(t, bool)
+    for block in (0, 7, 20):
+        high[16 * block:16 * block + 16] = True
+    q = np.zeros((1, 2, 64))
+    q[0, :, 0] = 1.0
+    k[0, :, 0, 0] = np.where(high, 20 * np.log(2) * 8, 0.0)      # a score of 20 ln 2 where high, else 0
+    k = k.astype(np.float32).astype(np.float64)
+    v = np.where(high[None, :, None, None], 0.0, v * 2.0 ** -apart / 64)
+    v = v.astype(np.float32).astype(np.float64)
+    kd, vd = torch.from_numpy(k).float().cuda(), torch.from_numpy(v).float().cuda()
+    c.ctx.append_kv8(fmt, 0, 1, kd, vd, c.ints([t]), c.table, c.codes, c.scales, None, 1, tok_start=c.ints([0, t]))
+    c.oracle_write(k, v, [t], [0], ring=False)
+    c.check()
+    out, lse = torch.zeros((1, 2, 64), device="cuda"), torch.zeros((1, 2), device="cuda")
+    idx, count = listed(c, [0], 1)
+    c.ctx.full_attn_kv8(fmt, 0, torch.from_numpy(q).float().cuda(), c.ints([t]), c.table, c.codes, c.scales, idx, count,
+                        out, lse, 1)
+    assert c.ctx.get_device_error() == 0
+    K, V = c.kv(0, 0, t)
+    want, _ = O.full_attention(q[0], K, V, t)
+    # numbers relative to the values' size, so that no bound rests on a fixed smallest one
+    unit = 2.0 ** -apart
+    bound = held_bound(q[0], K, V / unit, fmt, "f32", v_scales(c, 0, t) / unit) * unit
+    assert np.abs(want).max() > 2.0 ** -126
+    err = np.abs(out[0].double().cpu().numpy() - want)
+    assert np.all(err <= bound + 2.0 ** -148), (err / bound).max()
