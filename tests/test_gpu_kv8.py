@@ -1099,3 +1099,71 @@ def test_small_values_far_below_the_largest_weight(torch, fmt, apart):
     assert np.abs(want).max() > 2.0 ** -126
     err = np.abs(out[0].double().cpu().numpy() - want)
     assert np.all(err <= bound + 2.0 ** -148), (err / bound).max()
+
+
+# ------------------------------------------------------- the gated step over the 8-bit cache
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "f32")])
+@pytest.mark.parametrize("how", ["plain", "graph"])
+def test_local_gate_and_full_over_8_bits(torch, fmt, dtype, how):
+    """A decode step as a server composes it: the write into cache and ring, Local from the ring (the
+    model's type), the gate, Full over the 8-bit cache for the rows that the gate lists; from no row
+    to all of them, with the context's scratch shared by Local and Full."""
+    from tests._harness import BF16_ATOL, BF16_RTOL, F32_ATOL, F32_RTOL
+    B, t = 4, [70, 17, 33, 200]
+    c = Case(torch, fmt=fmt, dtype=dtype, rows=B, columns=14, sink=3, window=21)
+    atol, rtol = (BF16_ATOL, BF16_RTOL) if dtype == "bf16" else (F32_ATOL, F32_RTOL)
+    kept = [[np.zeros((c.hkv, 224, c.d)) for _ in range(B)] for _ in "kv"]    # the model's values
+    past = t
+    starts = c.starts(past)
+    new = [c.values(1, sum(past), c.hkv, c.d) for _ in "kv"]
+    c.ctx.append_kv8(fmt, 0, 1, new[0][1], new[1][1], c.ints(past), c.table, c.codes, c.scales, c.ring, B,
+                     tok_start=c.ints(starts))
+    c.oracle_write(new[0][0], new[1][0], past, [0] * B)
+    for b in range(B):
+        for kv in (0, 1):
+            kept[kv][b][:, :past[b]] = new[kv][0][0, starts[b]:starts[b + 1]].transpose(1, 0, 2)
+    q, k, v = (torch.zeros((B, h, c.d), dtype=c.kind, device="cuda") for h in (c.hq, c.hkv, c.hkv))
+    pos, scores = c.ints([0] * B), torch.zeros(B, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros((B, c.hq), device="cuda")
+    flags = torch.zeros(B, dtype=torch.uint8, device="cuda")
+    idx, count = c.ints([0] * B), c.ints([0])
+
+    def step():
+        c.ctx.append_kv8(fmt, 0, 1, k[None], v[None], pos, c.table, c.codes, c.scales, c.ring, B)
+        c.ctx.local_attn(0, q, pos, c.ring, out, lse, B)
+        c.ctx.gate(scores, 0.0, B, flags, idx, count)
+        c.ctx.full_attn_kv8(fmt, 0, q, pos, c.table, c.codes, c.scales, idx, count, out, lse, B)
+
+    graph = None
+    if how == "graph":
+        pos.copy_(c.ints([x + 1 for x in t]))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    for flagged in ([], [2], [0, 1, 2, 3], [3, 0], [1], []):
+        t = [x + 1 for x in t]
+        fresh = [c.values(*x.shape) for x in (q, k, v)]
+        for x, (_, y) in zip((q, k, v), fresh):
+            x.copy_(y)
+        pos.copy_(c.ints(t))
+        scores.copy_(torch.tensor([0.5 if b in flagged else -0.5 for b in range(B)]))
+        if graph is not None:
+            graph.replay()
+        else:
+            step()
+        assert c.ctx.get_device_error() == 0
+        c.oracle_write(fresh[1][0][None], fresh[2][0][None], [1] * B, [x - 1 for x in t])
+        c.check()
+        assert int(count.item()) == len(flagged) and idx.tolist()[:len(flagged)] == sorted(flagged)
+        qh = fresh[0][0]
+        check_rows(c, qh, out, lse, flagged, t)
+        for b in range(B):
+            for kv in (0, 1):
+                kept[kv][b][:, t[b] - 1] = fresh[1 + kv][0][b]
+            if b in flagged:
+                continue
+            want, wl = O.local_attention(qh[b], kept[0][b][:, :t[b]], kept[1][b][:, :t[b]], t[b], c.sink, c.window)
+            assert np.all(np.abs(out[b].double().cpu().numpy() - want) <= atol + rtol * np.abs(want)), b
+            assert np.all(np.abs(lse[b].double().cpu().numpy() - wl) <= atol + rtol * np.abs(wl)), b
