@@ -45,9 +45,9 @@
 //     bank: 8 rows of 16K tokens 49.2, 48.2 and 50.8 us, the mixed batch 188, 187
 //     and 195: the copy engine's time against shared memory's.)
 //
-// Bound by HBM for long rows (one of 128K tokens, 8 KV heads, d = 128: 48.8 us
-// for 270 MB, 5.5 TB/s with the start and the merge; 15 rows of 4K to 64K: 184 us,
-// 6.3 TB/s), by latency for short ones (two rows of 64: 4.2 us).
+// Bound by HBM for long rows (one of 128K tokens, 8 KV heads, d = 128: 49.6 us
+// for 269 MB, 5.4 TB/s with the start and the merge; 15 rows of 4K to 64K: 187 us,
+// 6.2 TB/s), by latency for short ones (two rows of 64: 4.0 us).
 #define ODA_PLAN_ROLLED
 
 #include "kv8.cuh"
@@ -496,7 +496,8 @@ struct __align__(16) Meta {
 template <typename T, int D>
 __device__ __forceinline__ void merge_parts(const Attn8Args& a, float* sm, int b, int g, int pbase,
                                             int nparts) {
-  // (13 saves a 128K row's 37 parts a round, 0.3 us, and costs shorter rows as much)
+  // (13 saves a 128K row's 37 parts a round, 0.3 us, and costs shorter rows as much. At G = 4,
+  // d = 128 `split` is 1: a region of 10K tokens beside shorter ones, cut into 53, takes 7 rounds.)
   constexpr int U = 8;
   const int tid = threadIdx.x, G = a.G;
   const int nch = G * D / 4;                                 // 16 .. 128 chunks
@@ -940,7 +941,8 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
 }
 
 // Stages per warp: two where two CTAs of them fit an SM beside the row arrays
-// of a large batch, else one.
+// of a large batch, else one. (32 heads over 8, d = 128, contexts for 52 rows and for 53: 8 rows
+// of 16K 43.4 and 44.7 us in e4m3, 46.9 and 47.3 in int8, 15 rows of 4K to 64K 142 and 134.)
 int stages_for(const oda_config& c) {
   const int G = c.hq / c.hkv;
   return Smem(G, c.head_dim, c.max_batch, 2).total <= 113 * 1024 - 128 ? 2 : 1;

@@ -15,8 +15,8 @@
 //   append, any number: a warp a unit, the new tokens requested before the
 //     block id; bound by HBM (16K tokens, 100 MB: about 17 us).
 //   read: a warp takes kReadUnits units of an item, whose codes are all
-//     requested before the first is turned into values: half of the item
-//     numbers may be empty, and finding an item costs two round trips. Bound by
+//     requested before the first is turned into values: more than half of the
+//     item numbers may be empty, and finding an item costs two round trips. Bound by
 //     HBM (8 x 16K tokens, 805 MB: 126 us, 6.4 TB/s).
 #include "kv8.cuh"
 

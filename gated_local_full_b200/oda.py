@@ -214,7 +214,7 @@ _FAST_CALLS = ("oda_append_kv8", "oda_read_kv8", "oda_full_attn_kv8", "oda_range
 
 
 def _fastcall():
-    """The calls of a decode loop's 8-bit cache, compiled (bind/fastcall.cpp): 4 to 5 us
+    """The calls of a decode loop's 8-bit cache, compiled (bind/fastcall.cpp): about 4 us
     a call against 8 to 12 through ctypes with the checks in Python."""
     global _fast
     if _fast is None:

@@ -45,7 +45,9 @@
  *     launches. Before the wait an attention kernel may read row ids,
  *     lengths and block-table entries (bypassing L1) only to choose which
  *     K/V lines to warm in L2 with bulk prefetches; these are read again
- *     after the wait, and a prefetch returns no value. With the flag
+ *     after the wait, and a prefetch returns no value. (The attention over
+ *     the 8-bit cache also divides its work by them then, and keeps the
+ *     division if they are the same after the wait.) With the flag
  *     ODA_ATTN_INPUTS_READY the caller states that those inputs and the K/V
  *     were complete earlier, and the kernel also stages its first K/V tiles
  *     before the wait (see that flag).
@@ -360,7 +362,7 @@ oda_status oda_full_attn_gated_static(const oda_config* cfg, int layer, const vo
  * may be rounded up to 15 times before its block is full, tokens written
  * together once. A value that is not finite makes its block's scale NaN, and
  * the whole block (of that head, K or V) reads back as NaN until it is started
- * anew.
+ * anew. (Within 2^-23 of the largest float32, code * scale may be infinite.)
  * Pointers to codes must be 16-byte aligned, to scales 8-byte aligned.
  *
  * Errors: an unknown format is ODA_ERR_DTYPE; calling with another device current
