@@ -648,17 +648,17 @@ __device__ __forceinline__ void partition(const Attn8Args& a, bool report, int* 
 __device__ __forceinline__ bool same_lists(const Attn8Args& a, const int* sinfo, const int* rowb,
                                            const int* rowt, const int* rowlo) {
   const int nr = sinfo[0];
-  bool same = __ldcg(a.count) == nr;
+  bool same = load_list(a.count) == nr;
 #pragma unroll 1
   for (int i = threadIdx.x & 31; i < nr; i += 32) {
     const int b = rowb[i];
-    const int t = __ldcg(a.seq_lens + b);
+    const int id = load_list(a.idx + i), t = load_list(a.seq_lens + b);
     int first = 1, last = t;
     if (a.range_lo) {
-      first = __ldcg(a.range_lo + b);
-      last = __ldcg(a.range_hi + b) - 1;
+      first = load_list(a.range_lo + b);
+      last = load_list(a.range_hi + b) - 1;
     }
-    same = same && __ldcg(a.idx + i) == b && t >= 1 && first == rowlo[i] && last == rowt[i] &&
+    same = same && id == b && t >= 1 && first == rowlo[i] && last == rowt[i] &&
            first >= 1 && last >= first && last <= t && (last - 1) / ODA_TILE < a.max_blocks;
   }
   return __all_sync(0xffffffffu, same);
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(W * 32, 2) attn_kv8_kernel(const Attn8Args a) 
         Cursor c;
         locate(rowstart, sinfo[0], a.hkv, k, c);
         const int col = (rowlo[c.i] - 1) / ODA_TILE + k - (c.s1 - c.nt);
-        const int blk = col < a.max_blocks ? __ldcg(a.block_table + (long long)rowb[c.i] * a.max_blocks + col) : -1;
+        const int blk = col < a.max_blocks ? load_list(a.block_table + (long long)rowb[c.i] * a.max_blocks + col) : -1;
         if (blk >= 0 && (long long)blk < a.num_blocks) {
           const long long th = (long long)blk * a.hkv + c.g;
           bulk_prefetch_l2(a.codes + th * TILE, TILE);

@@ -76,9 +76,9 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
       const int r = base + lane;
       int v_ts = 0, v_te = 0, v_t = 0;
       if (r < a.B) {
-        v_ts = __ldg(a.tok_start + r);
-        v_te = __ldg(a.tok_start + r + 1);
-        v_t = __ldg(a.seq_lens + r);
+        v_ts = load_int(a.tok_start + r);
+        v_te = load_int(a.tok_start + r + 1);
+        v_t = load_int(a.seq_lens + r);
       }
       const unsigned wrong = __ballot_sync(0xffffffffu, v_ts < 0 || v_te < v_ts || v_te > a.n_tokens);
       const unsigned who = ((wrong & (0u - wrong)) * 2u - 1u) &    // up to the first wrong one
@@ -101,7 +101,7 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
     if (n == 0) return false;
     j = (int)((long long)it - (ts / ODA_TILE + 2ll * b));
   } else {
-    m.t = __ldg(a.seq_lens + m.b);
+    m.t = load_int(a.seq_lens + m.b);
   }
   const long long past = m.t - n;               // positions before the call's
   if (m.t < 1 || past < 0) {
@@ -121,7 +121,7 @@ __device__ __forceinline__ bool find_item(const Kv8Args& a, unsigned it, Item& m
 // The physical block of a row's column, or -1 (recorded).
 __device__ __forceinline__ long long find_block(const Kv8Args& a, int b, int col) {
   const long long blk =
-      col < a.max_blocks ? __ldg(a.block_table + (long long)b * a.max_blocks + col) : -1;
+      col < a.max_blocks ? load_int(a.block_table + (long long)b * a.max_blocks + col) : -1;
   if (blk >= 0 && blk < a.num_blocks) return blk;
   record_error(a.err, ODA_ERR_BOUNDS);
   return -1;
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) append_one_kv8_kernel(const Kv8Args 
                          << ((threadIdx.x & 31) / R::LPR * R::LPR);
   const T* src = static_cast<const T*>(kv ? a.v_new : a.k_new) +
                  (((long long)l * a.n_tokens + b) * a.hkv + g) * D + li * R::EPL;
-  const uint4 x = __ldcs(reinterpret_cast<const uint4*>(src));
-  const int t = __ldg(a.seq_lens + b);
+  const uint4 x = load_stream(reinterpret_cast<const uint4*>(src));
+  const int t = load_int(a.seq_lens + b);
   if (t < 1) {
     record_error(a.err, ODA_ERR_BOUNDS);
     return;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 1024 : 512) / kThr
     // and the largest magnitude stays)
     const int s = p * R::RPP + rr;
     const int i = s >= m.s0 && s < m.s1 ? s - m.s0 : 0;
-    x[p] = __ldcs(reinterpret_cast<const uint4*>(src + (long long)i * a.hkv * D));
+    x[p] = load_stream(reinterpret_cast<const uint4*>(src + (long long)i * a.hkv * D));
   }
   const long long blk = find_block(a, m.b, m.col);
   if (blk < 0) return;
@@ -340,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, (D * sizeof(T) <= 256 ? 1024 : 768) 
       // (what is not wanted reads a wanted slot again: no branch between the loads)
       const uint8_t* src = tile + ((there ? u : 0) * ODA_TILE + (s >= m.s0 && s < m.s1 ? s : m.s0)) * D;
       if (NW == 2) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
+        const uint2 v = load_stream(reinterpret_cast<const uint2*>(src));
         c[u][p][0] = v.x;
         c[u][p][NW - 1] = v.y;
       } else {
-        c[u][p][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+        c[u][p][0] = load_stream(reinterpret_cast<const uint32_t*>(src));
       }
     }
   }

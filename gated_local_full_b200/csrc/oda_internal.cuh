@@ -191,6 +191,40 @@ __device__ __forceinline__ int ticket_add(int* p, int v) {
   return old;
 }
 
+// Loads of what the launch before may have written. The compiler keeps volatile
+// assembly in order, so a load written behind pdl_wait() stays behind it and one that is
+// made again is made again; __ldg (for memory that nothing writes while the kernel
+// lives, which with a dependent launch includes its predecessor's end) promises
+// neither. load_list bypasses L1 (a value read before the wait leaves no line there),
+// load_int goes through it (lists that many warps of an SM read), the others stream.
+__device__ __forceinline__ int load_list(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int load_int(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load_stream(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_stream(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // Asynchronous global -> shared copies that hold no registers (cp.async):
 // 16 bytes through L2 only, or 4 bytes; wait_all waits for this thread's.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

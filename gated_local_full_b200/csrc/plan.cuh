@@ -15,7 +15,7 @@
 //
 // plan_rows runs on warp 0 of a block and leaves the per-row arrays in shared
 // memory; plan_cta turns them into one CTA's share. Its global loads bypass
-// L1 (ld.global.cg), so a guess made before a dependency wait leaves no stale
+// L1 (load_list), so a guess made before a dependency wait leaves no stale
 // line behind for the loads after it. The attention kernel can
 // run both itself, or read a plan that another kernel wrote once for all the
 // launches that share it (the Local launches of a decode step).
@@ -62,8 +62,8 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
   // with B <= 32 every lane loads one row's length and one compacted id
   // before the count, so the three loads travel together instead of chaining
   const bool small = p.B <= 32;
-  const int tl = (small && lane < p.B) ? __ldcg(p.seq_lens + lane) : 0;
-  const int il = (small && !ring && lane < p.B) ? __ldcg(p.idx + lane) : 0;
+  const int tl = (small && lane < p.B) ? load_list(p.seq_lens + lane) : 0;
+  const int il = (small && !ring && lane < p.B) ? load_list(p.idx + lane) : 0;
   int nr;
   if (ring) {
     nr = p.B;
@@ -79,11 +79,11 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
   for (int base = 0; base < nr; base += 32) {
     const int i = base + lane;
     int nt = 0;
-    const int bl = i < nr ? (ring ? i : (small ? il : __ldcg(p.idx + i))) : 0;
+    const int bl = i < nr ? (ring ? i : (small ? il : load_list(p.idx + i))) : 0;
     const bool okl = bl >= 0 && bl < p.B;
     const int ts = __shfl_sync(0xffffffffu, tl, okl ? (bl & 31) : 0);   // all lanes shuffle
     if (i < nr) {
-      const int t = !okl ? 0 : (small ? ts : __ldcg(p.seq_lens + bl));
+      const int t = !okl ? 0 : (small ? ts : load_list(p.seq_lens + bl));
       int first = 1, last = t;                   // positions first..last are read
       if (!okl || t < 1) {
         if (p.report) record_error(p.err, ODA_ERR_BOUNDS);
@@ -92,7 +92,7 @@ __device__ __forceinline__ PlanHead plan_rows(const PlanIn& p, int* rowb, int* r
       } else {
         bool ok = true;
         if (p.range_lo) {                        // the region [lo, hi), within 1..t
-          const int rl = __ldcg(p.range_lo + bl), rh = __ldcg(p.range_hi + bl);
+          const int rl = load_list(p.range_lo + bl), rh = load_list(p.range_hi + bl);
           ok = rl >= 1 && rh > rl && rh - 1 <= t;
           first = rl;
           last = rh - 1;

@@ -1167,3 +1167,65 @@ def test_local_gate_and_full_over_8_bits(torch, fmt, dtype, how):
             want, wl = O.local_attention(qh[b], kept[0][b][:, :t[b]], kept[1][b][:, :t[b]], t[b], c.sink, c.window)
             assert np.all(np.abs(out[b].double().cpu().numpy() - want) <= atol + rtol * np.abs(want)), b
             assert np.all(np.abs(lse[b].double().cpu().numpy() - wl) <= atol + rtol * np.abs(wl)), b
+
+
+@pytest.mark.parametrize("late,one_each", [(k, False) for k in ("seq_lens", "block_table", "tok_start", "k_new")] +
+                         [(k, True) for k in ("seq_lens", "block_table", "k_new")])
+def test_a_write_and_a_read_of_what_the_launch_before_stores_late(torch, late_store, late, one_each):
+    """The write and the read are released early by the launch that stores one of their inputs: they
+    use it as it was stored, not as it was."""
+    B, new = 5, [1] * 5 if one_each else [3, 40, 0, 17, 1]
+    c = Case(torch, fmt="int8", dtype="f32", hq=1, hkv=1, d=64, rows=B, columns=6, sink=3, window=20)
+    past = [0, 9, 30, 16, 50]
+    c.write(past, [0] * B)
+    c.check()
+    t = [a + n for a, n in zip(past, new)]
+    total = sum(new)
+    (k, kd), (v, vd) = (c.values(1, total, 1, 64) for _ in "kv")
+    right = dict(seq_lens=c.ints(t), block_table=c.table.clone().flatten(), tok_start=c.ints(c.starts(new)),
+                 k_new=kd.clone().flatten().view(torch.int32))
+    wrong = dict(seq_lens=c.ints([5, 1, 96, 20, 7] if one_each else [40, 44, 0, 50, 96]),
+                 block_table=right["block_table"].flip(0).contiguous(),
+                 tok_start=c.ints([0, total, total, total, total, total]), k_new=torch.zeros_like(right["k_new"]))
+    held = {n: (wrong if n == late else right)[n].clone() for n in right}
+    out = [torch.full((1, total, 1, 64), 9.0, device="cuda") for _ in "kv"]
+    table = held["block_table"].view(B, 6)
+    starts = None if one_each else held["tok_start"]
+    torch.cuda.synchronize()
+    late_store(held[late], right[late])
+    c.ctx.append_kv8("int8", 0, 1, held["k_new"].view(torch.float32).view(1, total, 1, 64), vd, held["seq_lens"], table,
+                     c.codes, c.scales, c.ring, B, tok_start=starts)
+    c.oracle_write(k, v, new, past)
+    c.check()
+    if late != "k_new":
+        held[late].copy_(wrong[late])
+        torch.cuda.synchronize()
+        late_store(held[late], right[late])
+    c.ctx.read_kv8("int8", 0, 1, held["seq_lens"], table, c.codes, c.scales, out[0], out[1], B, tok_start=starts)
+    assert c.ctx.get_device_error() == 0
+    at = c.starts(new)
+    for b in range(B):
+        for o, x in zip(out, c.kv(0, b, t[b])):
+            want = x[0, t[b] - new[b]:].astype(np.float32)
+            assert np.array_equal(o[0, at[b]:at[b + 1], 0].cpu().numpy(), want), b
+
+
+@pytest.mark.parametrize("late", ["positions", "q", "inv_freq", "weight"])
+def test_a_rotation_of_what_the_launch_before_stores_late(torch, late_store, late):
+    c = Case(torch, dtype="f32", hq=2, hkv=1, d=64, rows=1, columns=1)
+    n = 40
+    f = (10000.0 ** (-np.arange(32) / 32.0)).astype(np.float32)
+    pos = c.r.integers(0, 1 << 17, n)
+    (q, qd), (w, wd) = c.values(n, 2, 64), c.values(64)
+    bits = lambda x: x.clone().flatten().view(torch.int32)  # noqa: E731
+    right = dict(positions=c.ints(pos), q=bits(qd), inv_freq=bits(torch.from_numpy(f).cuda()), weight=bits(wd))
+    held = {k: torch.zeros_like(x) if k == late else x.clone() for k, x in right.items()}
+    out = torch.full((n, 2, 64), 9.0, device="cuda")
+    torch.cuda.synchronize()
+    late_store(held[late], right[late])
+    c.ctx.qk_norm_rope(held["q"].view(torch.float32).view(n, 2, 64), None, held["weight"].view(torch.float32), None, 1e-5,
+                       held["inv_freq"].view(torch.float32), held["positions"], out, None)
+    want = O.norm_rotate(q, w, 1e-5, pos, f)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= rope_bound(q, w, 1e-5, pos, f, False, "f32"))
+    assert c.ctx.get_device_error() == 0
