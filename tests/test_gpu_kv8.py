@@ -892,51 +892,53 @@ def late_store(tmp_path_factory):
 
 @pytest.mark.parametrize("late,region", [(k, False) for k in ("t", "idx", "count", "table")] +
                          [(k, True) for k in ("t", "idx", "count", "lo", "hi", "table")])
-def test_a_list_written_late_by_the_launch_before(torch, late_store, late, region):
+@pytest.mark.parametrize("B,columns", [(5, 130), (40, 13)])
+def test_a_list_written_late_by_the_launch_before(torch, late_store, late, region, B, columns):
     """The launch before lets the attention start, and only then stores one of the lists: lengths
     that a region's end outgrows or that are refused as they were, ids and blocks out of range, counts
     of none and of too many, bounds of nothing. What was worked out from the old list must not be used, and
     the call after it, with nothing changed, gives the same bits (no ticket is left over)."""
-    c = Case(torch, fmt="int8", hq=4, hkv=2, rows=5, columns=130)
-    full_t = [2077, 900, 16, 515, 1300]
-    c.write(full_t, [0] * 5, ring=False)
-    q, qd = c.values(5, c.hq, c.d)
-    held = {k: c.ints([0] * (1 if k == "count" else 5)) for k in ("t", "idx", "count", "lo", "hi")}
+    c = Case(torch, fmt="int8", hq=4, hkv=2, rows=B, columns=columns)
+    full_t = [min(16 * columns, x) for x in ([2077, 900, 16, 515, 1300] * 8)[:B]]
+    c.write(full_t, [0] * B, ring=False)
+    q, qd = c.values(B, c.hq, c.d)
+    held = {k: c.ints([0] * (1 if k == "count" else B)) for k in ("t", "idx", "count", "lo", "hi")}
     held["table"] = c.table.flatten()
     blocks = c.table_h.reshape(-1).tolist()
     for step in range(10):
         t = [int(c.r.integers(x // 2 + 1, x + 1)) for x in full_t]
-        rows = [int(x) for x in c.r.permutation(5)[:1 + step % 5]]
+        rows = [int(x) for x in c.r.permutation(B)[:1 + step % 5 * (B // 5)]]
         hi = [x + 1 for x in t]                            # regions that end at the row's last position
         lo = [int(c.r.integers(1, h)) for h in hi]
-        new = dict(t=t, idx=rows + [-1] * (5 - len(rows)), count=[len(rows)], lo=lo, hi=hi, table=blocks)
-        old = dict(t=[[1] * 5, [x - 1 for x in t], [0] * 5, [x // 3 + 1 for x in t], [2 ** 31 - 1] * 5],
-                   idx=[[-1] * 5, [4, 3, 2, 1, 0], [7] * 5, [0] * 5, [2 ** 31 - 1] * 5],
-                   count=[[0], [5], [9], [-3], [1]],
-                   lo=[[0] * 5, [x + 1 for x in t], [1] * 5, [-5] * 5, [x // 2 for x in hi]],
-                   hi=[[0] * 5, [x + 1 for x in lo], [x + 2 for x in t], [-2 ** 31] * 5, [x // 2 + 1 for x in hi]],
-                   table=[blocks[::-1], [-1] * 650, [c.blocks] * 650, [0] * 650, blocks[130:] + blocks[:130]])
+        new = dict(t=t, idx=rows + [-1] * (B - len(rows)), count=[len(rows)], lo=lo, hi=hi, table=blocks)
+        old = dict(t=[[1] * B, [x - 1 for x in t], [0] * B, [x // 3 + 1 for x in t], [2 ** 31 - 1] * B],
+                   idx=[[-1] * B, list(range(B))[::-1], [B + 2] * B, [0] * B, [2 ** 31 - 1] * B],
+                   count=[[0], [B], [B + 4], [-3], [1]],
+                   lo=[[0] * B, [x + 1 for x in t], [1] * B, [-5] * B, [x // 2 for x in hi]],
+                   hi=[[0] * B, [x + 1 for x in lo], [x + 2 for x in t], [-2 ** 31] * B, [x // 2 + 1 for x in hi]],
+                   table=[blocks[::-1], [-1] * len(blocks), [c.blocks] * len(blocks), [0] * len(blocks),
+                          blocks[columns:] + blocks[:columns]])
         before = old[late][step % 5]
         device = {k: c.ints(v) for k, v in new.items()}
         for k in held:
             held[k].copy_(c.ints(before) if k == late else device[k])
-        out = torch.full((5, c.hq, c.d), 7.0, dtype=c.kind, device="cuda")
-        lse = torch.full((5, c.hq), 7.0, device="cuda")
+        out = torch.full((B, c.hq, c.d), 7.0, dtype=c.kind, device="cuda")
+        lse = torch.full((B, c.hq), 7.0, device="cuda")
         again, lse2 = out.clone(), lse.clone()
         torch.cuda.synchronize()
         late_store(held[late], device[late])
         for o, l in ((out, lse), (again, lse2)):
-            table = held["table"].view(5, 130)
+            table = held["table"].view(B, columns)
             if region:
                 c.ctx.range_attn_kv8(c.fmt, 0, qd, held["t"], held["lo"], held["hi"], table, c.codes, c.scales,
-                                     held["idx"], held["count"], o, l, 5)
+                                     held["idx"], held["count"], o, l, B)
             else:
                 c.ctx.full_attn_kv8(c.fmt, 0, qd, held["t"], table, c.codes, c.scales, held["idx"],
-                                    held["count"], o, l, 5)
+                                    held["count"], o, l, B)
         assert c.ctx.get_device_error() == 0, step
         check_rows(c, q, out, lse, rows, t, *((lo, hi) if region else ()))
         assert torch.equal(out, again) and torch.equal(lse, lse2), (step, before)
-        rest = [b for b in range(5) if b not in rows]
+        rest = [b for b in range(B) if b not in rows]
         assert (out[rest] == 7).all()
 
 
