@@ -195,11 +195,12 @@ __device__ __forceinline__ int ticket_add(int* p, int v) {
 // assembly in order, so a load written behind pdl_wait() stays behind it and one that is
 // made again is made again; __ldg (for memory that nothing writes while the kernel
 // lives, which with a dependent launch includes its predecessor's end) promises
-// neither. load_list bypasses L1 (a value read before the wait leaves no line there),
-// load_int goes through it (lists that many warps of an SM read), the others stream.
+// neither. load_list may be used before the wait, while the value is being written: it
+// bypasses L1 (and leaves no line there). load_int goes through L1 (lists that many warps
+// of an SM read), the others stream.
 __device__ __forceinline__ int load_list(const int32_t* p) {
   int v;
-  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ int load_int(const int32_t* p) {
